@@ -71,8 +71,11 @@ enum swiglu_status {
     SWIGLU_ERR_OVERLAP = 9,          /* an output overlaps an input         */
     SWIGLU_ERR_NO_DEVICE = 10,       /* no CUDA device is usable            */
     SWIGLU_ERR_BAD_FLAGS = 11,       /* unknown bit in swiglu_fwd_ex flags  */
-    SWIGLU_ERR_BAD_EPILOGUE = 12     /* unknown activation, non-finite gate
-                                        multiplier, or only one of G/U     */
+    SWIGLU_ERR_BAD_EPILOGUE = 12,    /* unknown activation, non-finite gate
+                                        multiplier, or only one of G/U;
+                                        non-finite residual scale, bad eps */
+    SWIGLU_ERR_BAD_BLOCK = 13,       /* block is not a swiglu_block         */
+    SWIGLU_ERR_WORKSPACE = 14        /* workspace missing or too small      */
 };
 
 /* Gate activations of the epilogue variants, h = act(alpha * g) * u. */
@@ -339,6 +342,156 @@ SWIGLU_API int swiglu_bwd_gemms(const void *dG, const void *dU, const void *Wg,
                                 const void *Wu, const void *X, void *dX,
                                 void *dWg, void *dWu, int64_t M, int64_t K,
                                 int64_t N, int dtype, cudaStream_t stream);
+
+/* Blocks of 128 of the e4m3 operands: one fp32 scale per ... */
+enum swiglu_block {
+    SWIGLU_BLOCK_ROW = 0,  /* 1 x 128 values of a row                        */
+    SWIGLU_BLOCK_TILE = 1  /* 128 x 128 values                               */
+};
+
+/*
+ * swiglu_quant_b128 -- e4m3 quantisation of X [R, C] in blocks of 128: the
+ * operands of swiglu_gemm_b128 and swiglu_fwd_b128.  For each block,
+ *   amax = max |x|,  e = the smallest integer with amax <= 448 * 2^e,
+ *   clamped to [-126, 127],  s = 2^e (1 for a block of zeros),
+ *   q = e4m3_rne(x / s)      (|x / s| <= 448; the division is exact).
+ * A block holding Inf or NaN: s = NaN and every code 0x7F (NaN).
+ *
+ *  X   [R, C] device, dtype elements, 16-byte aligned; C a multiple of 16.
+ *  Q   codes, one byte each, 16-byte aligned.  S fp32 scales, 16-byte aligned.
+ *  block, transpose -- R4, R16: R rounded up to 4, 16; CB = ceil(C/128),
+ *  RB = ceil(R/128):
+ *    ROW,  0:  Q [R, C],    S [CB, R4]: block b of row r at S[b*R4 + r] (the
+ *                           rows are innermost; entries r >= R not written)
+ *    TILE, 0:  Q [R, C],    S [RB, CB]
+ *    ROW,  1:  Q [C, R16]   the codes of X^T, blocks along R; columns >= R of
+ *                           Q are 0;  S [RB, C]: block b of column c at
+ *                           S[b*C + c], the ROW scales of a [C, R16] operand
+ *    TILE, 1:  Q [C, R16],  S [CB, RB]
+ *  (the transposes are the operands of a product that reduces over R: weight
+ *  gradients reduce over the tokens, input gradients over the weight's rows).
+ *  R == 0 or C == 0: nothing enqueued.  Q and S must not overlap X or each
+ *  other.  Allocates no device memory.
+ */
+SWIGLU_API int swiglu_quant_b128(const void *X, void *Q, float *S, int64_t R, int64_t C, int dtype,
+                                 int block, int transpose, cudaStream_t stream);
+
+/*
+ * swiglu_gemm_b128 -- product of block-scaled e4m3 operands:
+ *   Y[m,n] = sum_b As[m,b] Bs[n,b] sum_{k = 128b}^{128b+127} A[m,k] B[n,k]
+ * (b < KB = ceil(K/128); a last block shorter than 128 is allowed).
+ *
+ *  A   [M, K] device e4m3 codes, 16-byte aligned; K a multiple of 16.
+ *  As  1 x 128 scales of A: [KB, M4], M4 = M rounded up to 4, block b of row
+ *      m at As[b*M4 + m] (as swiglu_quant_b128 writes them).
+ *  B   [N, K] device e4m3 codes, 16-byte aligned; N a multiple of 8.
+ *  Bs  b_block SWIGLU_BLOCK_TILE: [ceil(N/128), KB] (weights);
+ *      SWIGLU_BLOCK_ROW: [KB, N], block b of row n at Bs[b*N + n].
+ *  Y   [M, N] device, out_dtype elements, 16-byte aligned; written only.
+ *
+ *  With X, W, dY quantised by swiglu_quant_b128, a linear layer Y = X W^T is
+ *  (X, W tile), its input gradient (dY, W tile transposed) and its weight
+ *  gradient (dY transposed, X transposed, b_block ROW).
+ *  Each block's products accumulate in fp32 on the tensor cores; the scaled
+ *  blocks are summed in fp32 with round-to-nearest adds in block order; one
+ *  rounding to out_dtype.  Any fp32 scales are taken as they are (negative,
+ *  zero, NaN and Inf follow the formula); NaN codes give NaN.
+ *  M == 0 or N == 0: nothing enqueued.  K == 0: Y is set to +0.  Y must not
+ *  overlap an input.  Allocates no device memory.
+ */
+SWIGLU_API int swiglu_gemm_b128(const void *A, const float *As, const void *B, const float *Bs,
+                                void *Y, int64_t M, int64_t N, int64_t K, int b_block,
+                                int out_dtype, cudaStream_t stream);
+
+/*
+ * swiglu_fwd_b128 -- the fused gate/up projection on block-scaled e4m3
+ * operands: H = act(alpha G) (.) U with G, U the swiglu_gemm_b128 products of
+ * X with Wg and Wu (weight scales in 128 x 128 tiles), one read of X, the
+ * activation on the fp32 sums.
+ *
+ *  X [M, K], Xs [KB, M4], Wg, Wu [N, K], Wgs, Wus [ceil(N/128), KB] as there.
+ *  H [M, N] device bf16, 16-byte aligned; N a multiple of 8, K of 16.
+ *  epi  as swiglu_fwd_epilogue (NULL: SiLU, alpha = 1); G and U bf16.
+ *  M == 0 or N == 0: nothing enqueued.  K == 0: H (and G, U) set to +0.
+ *  Outputs must not overlap an input or each other.  Allocates no device memory.
+ */
+SWIGLU_API int swiglu_fwd_b128(const void *X, const float *Xs, const void *Wg, const float *Wgs,
+                               const void *Wu, const float *Wus, void *H, int64_t M, int64_t K,
+                               int64_t N, const swiglu_epilogue *epi, cudaStream_t stream);
+
+/* Parameters of a block boundary; every pointer is device memory of the
+ * call's dtype, 16-byte aligned, or NULL. */
+typedef struct swiglu_block_norm_params {
+    const void *post_weight; /* W1 [D]: norm of the block's output; NULL: none   */
+    const void *pre_weight;  /* W2 [D]: norm of the residual sum; NULL: none     */
+    const void *gate;        /* g [gate_rows, D]; NULL: 1                        */
+    int64_t gate_rows;       /* divides M: row m uses gate row m/(M/gate_rows)
+                                (1: one gate per channel; the batch size: one
+                                per sequence; M: one per row); ignored without
+                                a gate                                       */
+    float residual_scale;    /* s, finite                                        */
+    float eps;               /* >= 0; added to the mean square                   */
+} swiglu_block_norm_params;
+
+/*
+ * swiglu_block_norm -- the boundary between two blocks in one pass over the
+ * residual stream: the norm of the finished block's output, its gate and
+ * residual scale, the residual sum, and the next block's input norm:
+ *   P  = W1 (.) Y * r1,    r1 = 1/sqrt(mean(Y^2) + eps)    (no W1: P = Y)
+ *   R' = R + s * g (.) P
+ *   N  = W2 (.) R' * r2,   r2 = 1/sqrt(mean(R'^2) + eps)   (no W2: no N)
+ * row by row, statistics and sums in fp32.  N is formed from R' before R' is
+ * rounded to dtype.
+ *
+ *  Y   [M, D] device, dtype elements: the block's output.
+ *  R   [M, D] device: the residual stream before the block.
+ *  Rn  [M, D] device: R'; may be R exactly (in place).
+ *  N   [M, D] device; may be Y exactly; not used without pre_weight.
+ *  rstd_post, rstd_pre  [M] device fp32, or NULL: r1 and r2, for the backward
+ *      (each not used without its weight).
+ *  D a multiple of 8 (bf16) / 4 (fp32), at most 16384 (bf16) / 8192 (fp32).
+ *  M == 0 or D == 0: nothing enqueued.  Any other overlap of an output with
+ *  an input or another output is SWIGLU_ERR_OVERLAP.  Allocates no device
+ *  memory.
+ */
+SWIGLU_API int swiglu_block_norm(const void *Y, const void *R, const swiglu_block_norm_params *p,
+                                 void *Rn, void *N, float *rstd_post, float *rstd_pre, int64_t M,
+                                 int64_t D, int dtype, cudaStream_t stream);
+
+/* Bytes of workspace swiglu_block_norm_bwd needs on the current device for
+ * these arguments (only whether p's pointers are NULL matters), or -1 for
+ * arguments it would reject. */
+SWIGLU_API int64_t swiglu_block_norm_bwd_workspace(const swiglu_block_norm_params *p, int64_t M,
+                                                   int64_t D, int dtype);
+
+/*
+ * swiglu_block_norm_bwd -- gradients of R' and N above:
+ *   n = R' r2, y = Y r1, a = W2 (.) dN,
+ *   dR = dR' + r2 (a - n mean(a (.) n)),
+ *   dY = r1 (b - y mean(b (.) y)),  b = s W1 (.) g (.) dR
+ *   d_pre = sum_m dN (.) n,  d_post = sum_m s g (.) dR (.) y,
+ *   d_gate[j] = s W1 (.) sum over gate row j's rows of dR (.) y
+ * (without W1: y = Y, dY = s g (.) dR; without W2: dR = dR').
+ *
+ *  dRn  [M, D] device: the gradient of R', or NULL for zero (then there must
+ *       be a dN).  dN [M, D]: the gradient of N; not used without pre_weight.
+ *  Y, Rn, rstd_post, rstd_pre, p  the forward's input, output (as rounded) and
+ *       statistics, and its parameters (eps is not used).
+ *  dY, dR [M, D]; d_post, d_pre [D]; d_gate [gate_rows, D]: written; the last
+ *       three only with their parameter, and then required.
+ *  workspace  16-byte aligned device memory of at least the bytes
+ *       swiglu_block_norm_bwd_workspace returns, scratch of this call alone
+ *       (calls that may run at once need one each); NULL if that is 0.
+ *  The column sums are fp32, summed in a fixed order (no atomics).  M == 0:
+ *  d_post, d_pre and d_gate set to +0.  No output may overlap an input,
+ *  another output or the workspace.
+ */
+SWIGLU_API int swiglu_block_norm_bwd(const void *dRn, const void *dN, const void *Y, const void *Rn,
+                                     const float *rstd_post, const float *rstd_pre,
+                                     const swiglu_block_norm_params *p, void *dY, void *dR,
+                                     void *d_post, void *d_pre, void *d_gate, void *workspace,
+                                     int64_t workspace_bytes, int64_t M, int64_t D, int dtype,
+                                     cudaStream_t stream);
 
 /* Route swiglu_fwd takes for these arguments (pure host function; returns a
  * swiglu_route, or -1 for arguments swiglu_fwd would reject). */

@@ -33,6 +33,11 @@ SWIGLU_ERR_OVERLAP = 9
 SWIGLU_ERR_NO_DEVICE = 10
 SWIGLU_ERR_BAD_FLAGS = 11
 SWIGLU_ERR_BAD_EPILOGUE = 12
+SWIGLU_ERR_BAD_BLOCK = 13
+SWIGLU_ERR_WORKSPACE = 14
+# enum swiglu_block
+SWIGLU_BLOCK_ROW = 0
+SWIGLU_BLOCK_TILE = 1
 # enum swiglu_activation
 SWIGLU_ACT_SILU = 0
 SWIGLU_ACT_GELU_TANH = 1
@@ -59,6 +64,15 @@ class Epilogue(ctypes.Structure):
                 ("G", ctypes.c_void_p), ("U", ctypes.c_void_p)]
 
 
+class BlockNormParams(ctypes.Structure):
+    """struct swiglu_block_norm_params."""
+    _fields_ = [("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_rows", ctypes.c_int64),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+_NORM = ctypes.POINTER(BlockNormParams)
+
 # name -> (restype, argtypes), mirroring include/swiglu.h
 SIGNATURES = {
     "swiglu_fwd": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
@@ -73,6 +87,14 @@ SIGNATURES = {
     "swiglu_bwd_dx_noalloc": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
     "swiglu_bwd_dw": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
     "swiglu_bwd_gemms": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P]),
+    "swiglu_quant_b128": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _I, _P]),
+    "swiglu_gemm_b128": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P]),
+    "swiglu_fwd_b128": (_I, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, ctypes.POINTER(Epilogue),
+                             _P]),
+    "swiglu_block_norm": (_I, [_P, _P, _NORM, _P, _P, _P, _P, _I64, _I64, _I, _P]),
+    "swiglu_block_norm_bwd_workspace": (_I64, [_NORM, _I64, _I64, _I]),
+    "swiglu_block_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _NORM, _P, _P, _P, _P, _P, _P, _I64, _I64,
+                                   _I64, _I, _P]),
     "swiglu_route_for": (_I, [_I64, _I64, _I64, _I]),
     "swiglu_last_route": (_I, []),
     "swiglu_status_string": (ctypes.c_char_p, [_I]),
@@ -329,6 +351,269 @@ def swiglu_bwd_gemms(dG: torch.Tensor, dU: torch.Tensor, Wg: torch.Tensor, Wu: t
                                 M, K, N, _dtype_code(dG), _stream(stream))
     _check("swiglu_bwd_gemms", st)
     return dX, dWg, dWu
+
+
+def _here(*tensors):
+    """All on the current device, whose stream and kernels the call uses."""
+    i = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"all tensors must be on the current device (cuda:{i})")
+
+
+def _codes(t: torch.Tensor, name: str):
+    _dev(t, name)
+    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn)")
+
+
+def _row_scales(s: torch.Tensor, name: str, rows: int, kb: int):
+    """The 1 x 128 scales [rows, kb], stored [kb, rows padded to 4]."""
+    if not s.is_cuda or s.dtype != torch.float32 or s.shape != (rows, kb):
+        raise ValueError(f"{name} must be a float32 CUDA tensor [{rows}, {kb}]")
+    if rows and kb and ((rows > 1 and s.stride(0) != 1) or
+                        (kb > 1 and s.stride(1) != (rows + 3) // 4 * 4)):
+        raise ValueError(f"{name} must be stored with its rows innermost, padded to a multiple of "
+                         "4 (as swiglu_quant_b128 returns it)")
+
+
+def swiglu_quant_b128(X: torch.Tensor, block: str = "row", transpose: bool = False, stream=None):
+    """e4m3 codes and fp32 power-of-two scales of X [..., C] (leading dims
+    flattened to R rows; bf16 or fp32; C a multiple of 16) in blocks of 128:
+    block "row" (1 x 128) or "tile" (128 x 128).  Returns (Q, S): Q torch.uint8
+    codes of X's shape, S [R, ceil(C/128)] ("row", rows innermost in memory) or
+    [ceil(R/128), ceil(C/128)].  transpose=True quantises X^T instead, blocks
+    along R: Q [C, R rounded up to 16] with zero codes behind R, S
+    [C, ceil(R/128)] or [ceil(C/128), ceil(R/128)]."""
+    _dev(X, "X")
+    if block not in ("row", "tile"):
+        raise ValueError('block must be "row" or "tile"')
+    _here(X)
+    tile = block == "tile"
+    code = _dtype_code(X)
+    C = X.shape[-1]
+    R = math.prod(X.shape[:-1])
+    dev = X.device
+    rows, cols = (C, (R + 15) // 16 * 16) if transpose else (R, C)
+    Q = torch.empty((rows, cols) if transpose else X.shape, dtype=torch.uint8, device=dev)
+    kb = (cols + 127) // 128
+    if tile:
+        S = torch.empty(((rows + 127) // 128, kb), dtype=torch.float32, device=dev)
+    else:
+        S = torch.empty((kb, (rows + 3) // 4 * 4), dtype=torch.float32, device=dev)
+    st = lib().swiglu_quant_b128(X.data_ptr(), Q.data_ptr(), S.data_ptr(), R, C, code,
+                                 1 if tile else 0, 1 if transpose else 0, _stream(stream))
+    if st:
+        _check("swiglu_quant_b128", st)
+    return Q, S if tile else S[:, :rows].t()
+
+
+def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: torch.Tensor,
+                     out_dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Y = A B^T of block-scaled e4m3 operands (swiglu_quant_b128 makes them):
+    A [..., K] codes with 1 x 128 scales As [M, KB], B [N, K] codes with scales
+    Bs [ceil(N/128), KB] (128 x 128 blocks) or [N, KB] (1 x 128, rows innermost
+    in memory); KB = ceil(K/128), K a multiple of 16, N of 8.  Y bf16 or fp32
+    with A's leading dims."""
+    _codes(A, "A")
+    _codes(B, "B")
+    K = A.shape[-1]
+    M = math.prod(A.shape[:-1])
+    N = B.shape[0]
+    if B.shape != (N, K):
+        raise ValueError(f"B must be [N, K] = [{N}, {K}]")
+    kb = (K + 127) // 128
+    _row_scales(As, "As", M, kb)
+    rows = (N + 127) // 128
+    if Bs.shape == (rows, kb):
+        block = SWIGLU_BLOCK_TILE
+        _dev(Bs, "Bs")
+        if Bs.dtype != torch.float32:
+            raise TypeError("Bs must be float32")
+    else:
+        block = SWIGLU_BLOCK_ROW
+        _row_scales(Bs, "Bs", N, kb)
+    code = _DT.get(out_dtype)
+    if code is None:
+        raise TypeError(f"unsupported out_dtype {out_dtype}; use bfloat16 or float32")
+    _here(A, As, B, Bs, Y)
+    if Y is None:
+        Y = torch.empty((*A.shape[:-1], N), dtype=out_dtype, device=A.device)
+    else:
+        _dev(Y, "Y")
+        if Y.dtype != out_dtype or Y.numel() != M * N:
+            raise ValueError("Y has the wrong dtype or size")
+    st = lib().swiglu_gemm_b128(A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(),
+                                Y.data_ptr(), M, N, K, block, code, _stream(stream))
+    if st:
+        _check("swiglu_gemm_b128", st)
+    return Y
+
+
+def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: torch.Tensor,
+                    Wu: torch.Tensor, Wus: torch.Tensor, H: torch.Tensor | None = None, stream=None,
+                    activation: int = SWIGLU_ACT_SILU, gate_multiplier: float = 1.0,
+                    return_gu: bool = False):
+    """swiglu_fwd on block-scaled e4m3 operands: X [..., K] codes with 1 x 128
+    scales Xs [M, KB], Wg, Wu [N, K] codes with 128 x 128 scales
+    [ceil(N/128), KB].  Returns H bf16 [..., N], or (H, G, U)."""
+    for t, n in ((X, "X"), (Wg, "Wg"), (Wu, "Wu")):
+        _codes(t, n)
+    K = X.shape[-1]
+    M = math.prod(X.shape[:-1])
+    N = Wg.shape[0]
+    if Wg.shape != (N, K) or Wu.shape != (N, K):
+        raise ValueError(f"weights must be [N, K] = [{N}, {K}]")
+    kb = (K + 127) // 128
+    _row_scales(Xs, "Xs", M, kb)
+    for t, n in ((Wgs, "Wgs"), (Wus, "Wus")):
+        _dev(t, n)
+        if t.dtype != torch.float32 or t.shape != ((N + 127) // 128, kb):
+            raise ValueError(f"{n} must be float32 [{(N + 127) // 128}, {kb}]")
+    _here(X, Xs, Wg, Wgs, Wu, Wus, H)
+    if H is None:
+        H = torch.empty((*X.shape[:-1], N), dtype=torch.bfloat16, device=X.device)
+    else:
+        _dev(H, "H")
+        if H.dtype != torch.bfloat16 or H.numel() != M * N:
+            raise ValueError("H has the wrong dtype or size")
+    G = U = None
+    if return_gu:
+        G = torch.empty_like(H)
+        U = torch.empty_like(H)
+    epi = Epilogue(int(activation), float(gate_multiplier), G.data_ptr() if return_gu else None,
+                   U.data_ptr() if return_gu else None)
+    st = lib().swiglu_fwd_b128(X.data_ptr(), Xs.data_ptr(), Wg.data_ptr(), Wgs.data_ptr(),
+                               Wu.data_ptr(), Wus.data_ptr(), H.data_ptr(), M, K, N,
+                               ctypes.byref(epi), _stream(stream))
+    if st:
+        _check("swiglu_fwd_b128", st)
+    return (H, G, U) if return_gu else H
+
+
+def _norm_params(like, M, D, post_weight, pre_weight, gate, residual_scale, eps):
+    """The checked parameter struct of the block norm calls."""
+    dt = like.dtype
+    for t, n in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if t is not None:
+            _dev(t, n)
+            if t.dtype != dt or t.shape != (D,):
+                raise ValueError(f"{n} must be [{D}] of Y's dtype")
+    rows = 1
+    if gate is not None:
+        _dev(gate, "gate")
+        if gate.dtype != dt or gate.shape[-1] != D or gate.dim() > 2:
+            raise ValueError(f"gate must be [{D}] or [rows, {D}] of Y's dtype")
+        rows = gate.numel() // D if D else 1
+    return BlockNormParams(post_weight.data_ptr() if post_weight is not None else None,
+                           pre_weight.data_ptr() if pre_weight is not None else None,
+                           gate.data_ptr() if gate is not None else None, rows,
+                           float(residual_scale), float(eps))
+
+
+def _same(t, like, name):
+    _dev(t, name)
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name} must have Y's dtype and shape")
+
+
+def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tensor | None = None,
+                      pre_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                      residual_scale: float = 1.0, eps: float = 1e-6, return_stats: bool = False,
+                      Rn: torch.Tensor | None = None, stream=None):
+    """The boundary between two blocks in one pass, for rows of D elements:
+    P = post_weight * Y / rms(Y), Rn = R + residual_scale * gate * P,
+    N = pre_weight * Rn / rms(Rn), rms(x) = sqrt(mean(x^2) + eps).  Y is the
+    block's output and R the residual stream [..., D] (bf16 or fp32).  Without
+    post_weight P = Y; without pre_weight N is None; gate is [D], or
+    [rows, D] with rows dividing the number of rows M (row m uses gate row
+    m // (M / rows)).  Returns (Rn, N), with return_stats=True (training)
+    (Rn, N, rstd_post, rstd_pre), fp32 [M], for swiglu_block_norm_bwd.  Rn may
+    be given as the output buffer, R itself included (in place)."""
+    _dev(Y, "Y")
+    _same(R, Y, "R")
+    code = _dtype_code(Y)
+    D = Y.shape[-1]
+    M = math.prod(Y.shape[:-1])
+    p = _norm_params(Y, M, D, post_weight, pre_weight, gate, residual_scale, eps)
+    _here(Y, R, post_weight, pre_weight, gate, Rn)
+    if Rn is None:
+        Rn = torch.empty_like(R)
+    else:
+        _same(Rn, Y, "Rn")
+    N = torch.empty_like(Y) if pre_weight is not None else None
+    r1 = r2 = None
+    if return_stats:
+        if post_weight is not None:
+            r1 = torch.empty((M,), dtype=torch.float32, device=Y.device)
+        if pre_weight is not None:
+            r2 = torch.empty((M,), dtype=torch.float32, device=Y.device)
+    st = lib().swiglu_block_norm(Y.data_ptr(), R.data_ptr(), ctypes.byref(p), Rn.data_ptr(),
+                                 N.data_ptr() if N is not None else None,
+                                 r1.data_ptr() if r1 is not None else None,
+                                 r2.data_ptr() if r2 is not None else None, M, D, code,
+                                 _stream(stream))
+    if st:
+        _check("swiglu_block_norm", st)
+    return (Rn, N, r1, r2) if return_stats else (Rn, N)
+
+
+def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: torch.Tensor,
+                          Rn: torch.Tensor, rstd_post: torch.Tensor | None,
+                          rstd_pre: torch.Tensor | None, post_weight: torch.Tensor | None = None,
+                          pre_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                          residual_scale: float = 1.0, stream=None):
+    """Gradients of swiglu_block_norm's Rn and N: returns (dY, dR, d_post,
+    d_pre, d_gate), the last three None without their parameter (d_gate has
+    gate's shape).  dRn or dN may be None for zero (dN only without
+    pre_weight); Rn, rstd_post, rstd_pre as the forward returned them."""
+    _dev(Y, "Y")
+    _same(Rn, Y, "Rn")
+    code = _dtype_code(Y)
+    D = Y.shape[-1]
+    M = math.prod(Y.shape[:-1])
+    if dRn is not None:
+        _same(dRn, Y, "dRn")
+    if (dN is None) != (pre_weight is None):
+        raise ValueError("dN and pre_weight go together")
+    if dN is not None:
+        _same(dN, Y, "dN")
+    for w, t, n in ((post_weight, rstd_post, "rstd_post"), (pre_weight, rstd_pre, "rstd_pre")):
+        if w is not None:
+            if t is None:
+                raise ValueError(f"{n} is missing")
+            _dev(t, n)
+            if t.dtype != torch.float32 or t.numel() != M:
+                raise ValueError(f"{n} must be float32 [{M}]")
+    p = _norm_params(Y, M, D, post_weight, pre_weight, gate, residual_scale, 0.0)
+    _here(dRn, dN, Y, Rn, rstd_post, rstd_pre, post_weight, pre_weight, gate)
+    dY = torch.empty_like(Y)
+    dR = torch.empty_like(Y)
+    dw1 = torch.empty_like(post_weight) if post_weight is not None else None
+    dw2 = torch.empty_like(pre_weight) if pre_weight is not None else None
+    dg = torch.empty_like(gate) if gate is not None else None
+    ref = ctypes.byref(p)
+    need = lib().swiglu_block_norm_bwd_workspace(ref, M, D, code)
+    ws = None
+    if need > 0:
+        # drawn on the current stream; a different stream of the call keeps it
+        ws = torch.empty((need,), dtype=torch.uint8, device=Y.device)
+    s = _stream(stream)
+    if ws is not None and stream is not None and s != torch.cuda.current_stream().cuda_stream:
+        ext = torch.cuda.ExternalStream(s, device=Y.device)
+        ext.wait_stream(torch.cuda.current_stream())  # its memory may still be in use there
+        ws.record_stream(ext)
+
+    def ptr(t):
+        return t.data_ptr() if t is not None else None
+
+    st = lib().swiglu_block_norm_bwd(ptr(dRn), ptr(dN), Y.data_ptr(), Rn.data_ptr(), ptr(rstd_post),
+                                     ptr(rstd_pre), ref, dY.data_ptr(), dR.data_ptr(), ptr(dw1),
+                                     ptr(dw2), ptr(dg), ptr(ws), max(need, 0), M, D, code, s)
+    if st:
+        _check("swiglu_block_norm_bwd", st)
+    return dY, dR, dw1, dw2, dg
 
 
 def swiglu_route_for(M: int, K: int, N: int, dtype: int) -> int:

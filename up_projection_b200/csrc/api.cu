@@ -11,6 +11,7 @@
 
 #include <mutex>
 
+#include "api_util.cuh"
 #include "kernels.cuh"
 #include "swiglu.h"
 
@@ -18,7 +19,6 @@ namespace swiglu {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxDim = (1LL << 31) - 1;  // TMA coordinates are 32-bit
 constexpr int kDecodeMaxM = 8;
 
 thread_local int t_last_route = SWIGLU_ROUTE_NONE;
@@ -27,7 +27,8 @@ std::mutex g_dev_mutex;
 DeviceInfo g_dev_cache[kMaxDevices];
 bool g_dev_valid[kMaxDevices];
 
-// Current device's properties; returns a status code.
+}  // namespace
+
 int current_device(DeviceInfo &out) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
@@ -63,14 +64,7 @@ int current_device(DeviceInfo &out) {
     return SWIGLU_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
-}
-
-int elem_size(int dtype) { return dtype == SWIGLU_BF16 ? 2 : 4; }
+namespace {
 
 // Shape/dtype rules of swiglu_fwd (no pointers involved).  Returns a status
 // code; on success *route is the route the call takes.
@@ -210,12 +204,6 @@ int check_bwd_dw(const void *dG, const void *dU, const void *X, const void *dWg,
             return SWIGLU_ERR_OVERLAP;
     }
     return SWIGLU_OK;
-}
-
-int from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return SWIGLU_OK;
-    (void)cudaGetLastError();
-    return SWIGLU_ERR_CUDA;
 }
 
 }  // namespace
@@ -533,6 +521,8 @@ SWIGLU_API const char *swiglu_status_string(int status) {
         case SWIGLU_ERR_NO_DEVICE: return "no usable CUDA device";
         case SWIGLU_ERR_BAD_FLAGS: return "unknown flag bit";
         case SWIGLU_ERR_BAD_EPILOGUE: return "bad epilogue (activation, multiplier or G/U pair)";
+        case SWIGLU_ERR_BAD_BLOCK: return "unknown scale block";
+        case SWIGLU_ERR_WORKSPACE: return "workspace missing or too small";
         default: return "unknown status";
     }
 }
@@ -560,7 +550,10 @@ SWIGLU_API int swiglu_sync_status(cudaStream_t stream) {
     if (e != cudaSuccess) return from_cuda(e);
     e = gemm_tf32x3_2sm_status_fetch_and_clear(&w8, stream);
     if (e != cudaSuccess) return from_cuda(e);
-    return (w1 | w2 | w3 | w4 | w5 | w6 | w7 | w8) ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
+    unsigned int w9 = 0;
+    e = gemm_b128_status_fetch_and_clear(&w9, stream);
+    if (e != cudaSuccess) return from_cuda(e);
+    return (w1 | w2 | w3 | w4 | w5 | w6 | w7 | w8 | w9) ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
 }
 
 SWIGLU_API int swiglu_selftest_wait_timeout(cudaStream_t stream) {

@@ -151,6 +151,38 @@ cudaError_t selftest_status_fetch_and_clear(unsigned int *host_out, cudaStream_t
 // clock cycles) never completes and gives up.
 cudaError_t launch_selftest_wait(long long limit_cycles, cudaStream_t stream);
 
+// Block-boundary norms (block_norm.cu).  Weights and gate may be null;
+// gate_rows rows of the gate are shared by M / gate_rows consecutive rows each.
+struct BlockNorm {
+    const void *w1 = nullptr;    // norm of the block's output
+    const void *w2 = nullptr;    // norm of the residual sum
+    const void *gate = nullptr;
+    int64_t gate_rows = 1;
+    float scale = 1.0f, eps = 0.0f;
+};
+cudaError_t launch_block_norm(const void *Y, const void *R, const BlockNorm &n, void *Rn, void *N,
+                              float *rstd1, float *rstd2, int64_t M, int D, int f32,
+                              const DeviceInfo &dev, cudaStream_t stream);
+// Bytes of the workspace a backward call needs (0: none).
+size_t block_norm_bwd_workspace(int64_t M, int D, int f32, const BlockNorm &n, int sm_count);
+cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y, const void *Rn,
+                                  const float *rstd1, const float *rstd2, const BlockNorm &n,
+                                  void *dY, void *dR, void *dw1, void *dw2, void *dgate,
+                                  void *workspace, int64_t M, int D, int f32,
+                                  const DeviceInfo &dev, cudaStream_t stream);
+
+// e4m3 quantisation in blocks of 128 (quant_b128.cu) and the products of
+// such operands (gemm_b128.cu).
+cudaError_t launch_quant_b128(const void *X, void *Q, float *S, int64_t R, int C, int f32,
+                              bool tile, bool trans, cudaStream_t stream);
+cudaError_t launch_gemm_b128(const void *A, const float *As, const void *B, const float *Bs,
+                             void *Y, int M, int N, int K, bool row_scales, int f32_out,
+                             const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_fwd_b128(const void *X, const float *Xs, const void *Wg, const float *Gs,
+                            const void *Wu, const float *Us, void *H, int M, int N, int K,
+                            const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t gemm_b128_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream);
+
 // Tensor-map encoding through the driver entry point (no libcuda link).
 bool tensor_maps_available();
 
