@@ -54,8 +54,8 @@ constexpr int kBlockK = 128;                 // bytes = e4m3 values per block an
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 4);  // (register shares go by groups of 4 warps)
 // 384 threads start with 168 registers each; the accumulating warps take
-// what the third group of warps gives back: 256 * 216 + 128 * 72 = 384 * 168.
-constexpr int kRegsLaunch = 168, kRegsEpi = 216, kRegsRest = 72;
+// what the third group of warps gives back: 256 * 232 + 128 * 40 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsEpi = 232, kRegsRest = 40;
 static_assert(256 * kRegsEpi + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
 constexpr int kMaxUnits = 32;                // units of 8 columns per tile
 constexpr int kMaxStages = 24;
@@ -91,6 +91,30 @@ struct Out {
     int act;
     float alpha;
 };
+
+// mbar_wait for waits that are long by design: after one test the thread
+// sleeps until the phase completes (or 20 us have passed) instead of polling,
+// which leaves the issue slots to the accumulating warps.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -140,6 +164,10 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // A warp's 32 rows x 64 bytes to global memory through its staging buffer:
 // lane = row writes its four 16-byte chunks (swizzled over the banks), then
 // every four lanes store 64 consecutive bytes of a row.  `cols16` of the four
@@ -158,6 +186,114 @@ __device__ __forceinline__ void store_rows(uint32_t buf, int lane, const uint4 (
         if (r < rows && j < cols16) *reinterpret_cast<uint4 *>(dst + r * row_bytes + j * 16) = w;
     }
     __syncwarp();
+}
+
+// One block's 32 accumulator columns of a warp, times their scales, into the
+// running sums.  Tile scales: the four units of 8 columns take slo below
+// unit `cut` (counted from these columns) and shi from there on.
+__device__ __forceinline__ void add_tile(unsigned long long (&acc)[16], const uint32_t (&v)[32],
+                                         float slo, float shi, int cut) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float s = u < cut ? slo : shi;
+        const unsigned long long s2 = pair2(s, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma2(acc[4 * u + i], v[8 * u + 2 * i], v[8 * u + 2 * i + 1], s2);
+    }
+}
+
+// The same with one scale for all 32 columns.
+__device__ __forceinline__ void add_block(unsigned long long (&acc)[16], const uint32_t (&v)[32], float s) {
+    const unsigned long long s2 = pair2(s, s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) fma2(acc[i], v[2 * i], v[2 * i + 1], s2);
+}
+
+// Row scales: one per column, in shared memory at sb.
+__device__ __forceinline__ void add_rows(unsigned long long (&acc)[16], const uint32_t (&v)[32],
+                                         float sa, uint32_t sb) {
+    const unsigned long long sa2 = pair2(sa, sa);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 w = lds_v4(sb + 16u * i);
+        const unsigned long long s0 = pair2(__uint_as_float(w.x), __uint_as_float(w.y));
+        const unsigned long long s1 = pair2(__uint_as_float(w.z), __uint_as_float(w.w));
+        fma2(acc[2 * i], v[4 * i], v[4 * i + 1], mul2(s0, sa2));
+        fma2(acc[2 * i + 1], v[4 * i + 2], v[4 * i + 3], mul2(s1, sa2));
+    }
+}
+
+// A warp's share of a tile, from its sums to global memory: rows row0 .. (at
+// most 32, `rows` of them), columns colg .. of `mine` units of 8.  acc[0..3]:
+// groups of 32 columns (gated: 0, 1 of G and 2, 3 of U).
+template <int kMode>
+__device__ __forceinline__ void store_tile(const unsigned long long (&acc)[4][16], const Out &out,
+                                           uint32_t buf, int lane, int64_t row0, int64_t colg, int N,
+                                           int rows, int mine) {
+    auto put_bf16 = [&](void *y, int group, int units_left, auto value) {
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[c] = make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3));
+        store_rows(buf, lane, v, static_cast<char *>(y) + 2 * (row0 * N + colg + 32 * group), 2ll * N,
+                   rows, units_left);
+    };
+    if constexpr (kMode == kGated) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int left = mine - 4 * j;
+            if (left > 0) {
+                put_bf16(out.y, j, left, [&](int i) {
+                    return pack_bf16x2(
+                        act::gated<false>(out.act, out.alpha, lo2(acc[j][i]), lo2(acc[2 + j][i])),
+                        act::gated<false>(out.act, out.alpha, hi2(acc[j][i]), hi2(acc[2 + j][i])));
+                });
+                if (out.g) {
+                    put_bf16(out.g, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+                    put_bf16(out.u, j, left,
+                             [&](int i) { return pack_bf16x2(lo2(acc[2 + j][i]), hi2(acc[2 + j][i])); });
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = mine - 4 * j;
+            if (left > 0) {
+                if (!out.f32) {
+                    put_bf16(out.y, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 16 columns = 64 bytes each
+                        uint4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const unsigned long long a0 = acc[j][8 * h + 2 * c], a1 = acc[j][8 * h + 2 * c + 1];
+                            v[c] = make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
+                                              static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32));
+                        }
+                        store_rows(buf, lane, v,
+                                   static_cast<char *>(out.y) + 4 * (row0 * N + colg + 32 * j + 16 * h),
+                                   4ll * N, rows, 2 * (left - 2 * h));
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Tile scales.  A tile's columns span at most three blocks of 128 (gated: two
+// of each weight); per block of the reduction the slot holds, behind the 128
+// row scales, four values: plain, of blocks b0 .. b0 + 3 (the last one
+// repeated), gated, of blocks b0, b0 + 1 of Wg and of Wu.  The scales' warp
+// fetches them ahead of the copies' pace (lanes 0..3, one table row each).
+template <int kMode>
+__device__ __forceinline__ const float *tile_scale_source(const float *bs0, const float *bs1, int b0,
+                                                          int lane, int N, int num_kb) {
+    const int blocks = (N + 127) / 128;
+    const int i = kMode == kGated ? (lane & 1) : (lane & 3);
+    const float *table = (kMode == kGated && (lane & 2)) ? bs1 : bs0;
+    return table + static_cast<int64_t>(min(b0 + i, blocks - 1)) * num_kb;
 }
 
 // tm_b*: rows of B (gated: of Wg and Wu), boxes of 8 q (lo) and 8 (q + 1)
@@ -531,6 +667,488 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Pairs of SMs (M > 128): each MMA covers 256 rows over the two CTAs of a
+// cluster (tcgen05 cta_group::2).  A CTA holds its own 128 rows of A and half
+// of the tile's rows of B (gated: the even CTA the rows of Wg, the odd one
+// those of Wu), so a stage is 32 KB instead of 48 and both the copies' writes
+// and the MMAs' reads of shared memory shrink by a third; each CTA accumulates
+// its own 128 rows.  The even CTA issues the MMAs; three threads of each CTA
+// issue its copies (B; A; the scales), one copy per block each, since one
+// thread issuing all of them took longer than a block's MMAs.
+
+constexpr int kPairStages = 6;
+constexpr int kSlotBlocks = 4;    // blocks of the reduction per slot of scales
+constexpr int kPairBufCols = 256;
+constexpr uint32_t kPairStageBytes = 32 * 1024;
+constexpr int kPairMaxSlots = 4;
+constexpr uint32_t kPairBars = 2 * kPairStages + 2 * kPairMaxSlots + 2 * 2 + 1;
+
+template <int kMode>
+struct PairLayout {
+    // per slot: row scales of A [4][128], then of B [4][s_cols], or the tile
+    // scales [4][4]
+    static constexpr int kSlots = kMode == kRowScales ? 2 : 4;
+    static constexpr uint32_t kOffB = kSlotBlocks * 512;
+    static constexpr uint32_t kSlotBytes = kOffB + kSlotBlocks * (kMode == kRowScales ? 1024 : 32);
+    static constexpr uint32_t kOffSlots = kPairStages * kPairStageBytes;
+    static constexpr uint32_t kOffOut = kOffSlots + kSlots * kSlotBytes;
+    static constexpr uint32_t kOffBar = kOffOut + kEpiWarps * kStageOutBytes;
+    static constexpr uint32_t kSmem = kOffBar + 8 * kPairBars + 32 + 1024;
+    static_assert(kSmem <= kMaxSmem, "exceeds the 227 KB opt-in shared memory");
+};
+
+struct PairPlan {
+    int tiles_m, tiles_n;
+    int groups;      // of 32 output columns
+    int half_rows;   // rows of B per CTA and stage: half the MMA's N
+    int s_cols;      // row scales of B per block
+    int num_kb;
+};
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    const uint32_t z = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;"
+        "\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(z)
+        : "memory");
+}
+
+// tm_b: rows of B (gated: of Wg), tm_u: of Wu, boxes of half_rows rows.
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    swiglu_gemm_b128_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
+                                 const __grid_constant__ CUtensorMap tm_as,
+                                 const __grid_constant__ CUtensorMap tm_b,
+                                 const __grid_constant__ CUtensorMap tm_u,
+                                 const __grid_constant__ CUtensorMap tm_bs,
+                                 const float *__restrict__ bs0, const float *__restrict__ bs1,
+                                 const Out out, int M, int N, const PairPlan p) {
+    using L = PairLayout<kMode>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const uint32_t bar_full = base + L::kOffBar;
+    const uint32_t bar_empty = bar_full + 8 * kPairStages;
+    const uint32_t bar_sfull = bar_empty + 8 * kPairStages;
+    const uint32_t bar_sempty = bar_sfull + 8 * kPairMaxSlots;
+    const uint32_t bar_tfull = bar_sempty + 8 * kPairMaxSlots;
+    const uint32_t bar_tempty = bar_tfull + 16;
+    const uint32_t bar_drain = bar_tempty + 16;
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(gbase + L::kOffBar + 8 * kPairBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::kOffBar + 8 * kPairBars + 16);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);  // (known uniform)
+    const int lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int pair = static_cast<int>(blockIdx.x) / 2;
+    const int num_pairs = static_cast<int>(gridDim.x) / 2;
+    const int num_tiles = p.tiles_m * p.tiles_n;
+    const int num_kb = p.num_kb;
+    const uint32_t a_bytes = kBM * 128u;
+    const uint32_t b_bytes = static_cast<uint32_t>(p.half_rows) * 128u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(bar_sfull + 8 * s, 1);
+            mbar_init(bar_sempty + 8 * s, kEpiWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 2 * kEpiWarps);  // both CTAs' warps
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_as);
+        tma_prefetch_desc(kMode == kGated && rank == 1 ? &tm_u : &tm_b);
+        if (kMode == kRowScales) tma_prefetch_desc(&tm_bs);
+    }
+    if (warp == kEpiWarps + 1) {
+        tmem_alloc_pair(smem_u32(tmem_ptr), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    // both CTAs' barriers initialised and TMEM allocated before any copy,
+    // arrive or MMA that reaches the other CTA
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_ptr);
+
+    // tile t: the CTA's rows m0 .., the tile's groups g0 .. g0 + cnt of 32 columns
+    auto tile_of = [&](int t, int &m0, int &g0, int &cnt) {
+        int mt, nt;
+        tile_coords<kGroupM / 2>(t, p.tiles_m, p.tiles_n, mt, nt);
+        m0 = mt * 2 * kBM + static_cast<int>(rank) * kBM;
+        g0 = static_cast<int>(static_cast<long long>(p.groups) * nt / p.tiles_n);
+        cnt = static_cast<int>(static_cast<long long>(p.groups) * (nt + 1) / p.tiles_n) - g0;
+    };
+
+    bool failed = false;
+
+    if (warp >= kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if ((warp == kEpiWarps || warp == kEpiWarps + 2) && lane == 0) {
+            // ----------------------- TMA producers: B (and the bytes of all), A
+            const bool is_b = warp == kEpiWarps;
+            const uint32_t full_r0 = map_to_rank(bar_full, 0);
+            const CUtensorMap *tm = !is_b ? &tm_a : (kMode == kGated && rank == 1 ? &tm_u : &tm_b);
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
+                int m0, g0, cnt;
+                tile_of(t, m0, g0, cnt);
+                const int row = !is_b ? m0 : 32 * g0 + (kMode == kGated ? 0 : static_cast<int>(rank) * p.half_rows);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait_long(bar_empty + 8 * stage, phase ^ 1u, abort_flag)) {
+                        failed = true;
+                        break;
+                    }
+                    // every copy of both CTAs is counted on the even CTA's barrier
+                    if (is_b && rank == 0) mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * (a_bytes + b_bytes));
+                    tma_load_2d_pair(tm, full_r0 + 8 * stage,
+                                     base + stage * kPairStageBytes + (is_b ? a_bytes : 0u), kb * kBlockK, row);
+                    ++issued;
+                    if (++stage == kPairStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // Never leave while a load may still write shared memory: the even
+            // CTA's barriers count both CTAs' copies, and every block of the
+            // odd CTA is consumed by the pair's MMAs before the last barrier.
+            for (int s = 0; s < kPairStages && rank == 0; ++s)
+                if (issued > s)
+                    mbar_wait_drain(bar_full + 8 * s,
+                                    static_cast<uint32_t>(((issued - 1 - s) / kPairStages) & 1));
+        }
+        if (warp == kEpiWarps + 3) {
+            // ------------------------------------------------------ scales
+            int slot = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
+                int m0, g0, cnt;
+                tile_of(t, m0, g0, cnt);
+                const float *src = nullptr;
+                if (kMode != kRowScales && lane < 16)  // lane: block lane / 4 of the slot, value lane % 4
+                    src = tile_scale_source<kMode>(bs0, bs1, g0 / 4, lane & 3, N, num_kb);
+                for (int kb = 0; kb < num_kb; kb += kSlotBlocks) {
+                    float v = 0.0f;
+                    if (kMode != kRowScales && lane < 16) v = __ldg(src + min(kb + lane / 4, num_kb - 1));
+                    if (!mbar_wait_long(bar_sempty + 8 * slot, phase ^ 1u, abort_flag)) {
+                        failed = true;
+                        break;
+                    }
+                    const uint32_t sb = bar_sfull + 8 * slot;
+                    const uint32_t dst = base + L::kOffSlots + slot * L::kSlotBytes;
+                    if (kMode != kRowScales) {
+                        if (lane < 16) sts_f32(dst + L::kOffB + 4u * lane, v);
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        // (blocks past the last arrive as zeros)
+                        mbar_arrive_expect_tx(sb, kSlotBlocks * (512u + (kMode == kRowScales ? 4u * p.s_cols : 0u)));
+                        tma_load_2d(&tm_as, sb, dst, m0, kb);
+                        if (kMode == kRowScales) tma_load_2d(&tm_bs, sb, dst + L::kOffB, 32 * g0, kb);
+                    }
+                    ++issued;
+                    if (++slot == L::kSlots) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < L::kSlots; ++s)
+                if (issued > s)
+                    mbar_wait_drain(bar_sfull + 8 * s,
+                                    static_cast<uint32_t>(((issued - 1 - s) / L::kSlots) & 1));
+        }
+        if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {
+            // ------------------------------------------ MMA issuer (pair)
+            const uint32_t idesc = make_idesc(0u, 2 * kBM, static_cast<uint32_t>(2 * p.half_rows));
+            const uint32_t empty_r1 = map_to_rank(bar_empty, 1);
+            const uint32_t tfull_r1 = map_to_rank(bar_tfull, 1);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait_long(bar_full + 8 * stage, phase, abort_flag) ||
+                        !mbar_wait_long(bar_tempty + 8 * buf, bphase ^ 1u, abort_flag)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = base + stage * kPairStageBytes;
+                    const uint64_t ad = sw128_kmajor_desc(a), bd = sw128_kmajor_desc(a + a_bytes);
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kPairBufCols);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8_pair(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
+                    mma_commit_pair(bar_empty + 8 * stage);
+                    mma_commit_pair(empty_r1 + 8 * stage);
+                    mma_commit_pair(bar_tfull + 8 * buf);
+                    mma_commit_pair(tfull_r1 + 8 * buf);
+                    if (++stage == kPairStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == 2) {
+                        buf = 0;
+                        bphase ^= 1u;
+                    }
+                }
+            }
+            // Every MMA issued here must finish before TMEM is released.
+            mma_commit_pair(bar_drain);
+            mbar_wait_drain(bar_drain, 0);
+        }
+    } else {
+        // ------------------------------------------ accumulation + epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t obuf = base + L::kOffOut + static_cast<uint32_t>(warp) * kStageOutBytes;
+        const uint32_t tempty_r0 = map_to_rank(bar_tempty, 0);
+        int slot = 0, buf = 0;
+        uint32_t sphase = 0, bphase = 0;
+        for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
+            int m0, g0, cnt;
+            tile_of(t, m0, g0, cnt);
+            // this warp's groups of 32 columns: the lower or upper half of the
+            // tile's (gated: of both products)
+            const int first = half ? (cnt + 1) / 2 : 0;
+            const int mine = half ? cnt / 2 : (cnt + 1) / 2;
+            const int rows = min(32, M - m0 - 32 * quad);  // <= 0: none
+            const uint32_t col0 = 32u * static_cast<uint32_t>(first);
+            const uint32_t col2 = kMode == kGated ? col0 + static_cast<uint32_t>(p.half_rows) : col0 + 64u;
+            // groups are read in pairs, in this order: plain 0 1 2 3, gated 0 2
+            // 1 3 (an odd count reads one more, whose sums are not stored)
+            const int groups = rows <= 0 ? 0 : (kMode == kGated ? 2 * mine : (mine + 1) / 2 * 2);
+            constexpr int kOrder[4] = {0, kMode == kGated ? 2 : 1, kMode == kGated ? 1 : 2, 3};
+            unsigned long long acc[4][16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
+            // each group's tile scale within its block's four
+            uint32_t at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                at[j] = 4u * static_cast<uint32_t>((g0 + first + (kMode == kGated ? (j & 1) : j)) / 4 - g0 / 4 +
+                                                   (kMode == kGated ? (j & 2) : 0));
+
+            float sa = 0.0f, sb[4] = {};
+            uint32_t srow = 0;        // this block's row scales of B
+            uint32_t v[2][32];
+            // One block ahead: wait for its accumulators, start reading them,
+            // and fetch its scales.
+            auto open_block = [&](int kb) -> bool {
+                if (kb % kSlotBlocks == 0 && !mbar_wait_long(bar_sfull + 8 * slot, sphase, abort_flag)) return false;
+                if (!mbar_wait_long(bar_tfull + 8 * buf, bphase, abort_flag)) return false;
+                tc_fence_after();
+                if (groups == 0) return true;
+                tmem_ld_32x32b_x32(lanes + static_cast<uint32_t>(buf * kPairBufCols) + col0, v[0]);
+                const uint32_t src = base + L::kOffSlots + slot * L::kSlotBytes;
+                const uint32_t blk = static_cast<uint32_t>(kb % kSlotBlocks);
+                sa = lds_f32(src + blk * 512u + 4u * (quad * 32 + lane));
+                if constexpr (kMode != kRowScales) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sb[j] = lds_f32(src + L::kOffB + blk * 16u + at[j]);
+                } else {
+                    srow = src + L::kOffB + blk * 4u * static_cast<uint32_t>(p.s_cols);
+                }
+                return true;
+            };
+            if (!open_block(0)) {
+                failed = true;
+                break;
+            }
+            for (int kb = 0; kb < num_kb; ++kb) {
+                const uint32_t d = lanes + static_cast<uint32_t>(buf * kPairBufCols);
+                float s[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] = sa * sb[j];
+                const float sa_now = sa;
+                const uint32_t srow_now = srow;
+                auto read = [&](int o) {
+                    const int g = kOrder[o];
+                    tmem_ld_32x32b_x32(d + (g < 2 ? col0 : col2) + 32u * (g & 1), v[o & 1]);
+                };
+                auto add = [&](int o) {
+                    const int g = kOrder[o];
+                    if constexpr (kMode == kRowScales)
+                        add_rows(acc[g], v[o & 1], sa_now, srow_now + 4u * ((g < 2 ? col0 : col2) + 32u * (g & 1)));
+                    else
+                        add_block(acc[g], v[o & 1], s[g]);
+                };
+                // the next 32 columns are on their way while these are added
+                if (groups > 0) {
+                    tmem_ld_wait(v[0]);
+                    read(1);
+                    add(0);
+                    if (groups > 2) {
+                        tmem_ld_wait(v[1]);
+                        read(2);
+                        add(1);
+                        tmem_ld_wait(v[0]);
+                        read(3);
+                        add(2);
+                    }
+                    tmem_ld_wait(v[1]);
+                }
+                // every value of this buffer has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty_r0 + 8 * buf);
+                if (++buf == 2) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+                const bool slot_done = kb % kSlotBlocks == kSlotBlocks - 1 || kb + 1 == num_kb;
+                const uint32_t slot_bar = bar_sempty + 8 * slot;
+                if (slot_done && ++slot == L::kSlots) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
+                if (kb + 1 < num_kb && !open_block(kb + 1)) {
+                    failed = true;
+                    break;
+                }
+                if (groups > 2) add(3);
+                else if (groups > 0) add(1);
+                if (slot_done) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(slot_bar);
+                }
+            }
+            if (failed || groups == 0) continue;
+            // (units of 8 columns: the last group may reach past N)
+            const int64_t colg = 32 * (static_cast<int64_t>(g0) + first);
+            const int left = static_cast<int>((N - colg) / 8);
+            store_tile<kMode>(acc, out, obuf, lane, m0 + 32 * quad, colg, N, rows, min(4 * mine, left));
+        }
+    }
+
+    if (failed) atomicOr(&g_gemm_b128_status, 1u);
+
+    tc_fence_before();
+    __syncthreads();
+    // the pair's MMAs have completed (the issuer drained them) and both CTAs'
+    // sums are stored before either frees TMEM or leaves
+    cluster_sync_all();
+    if (warp == kEpiWarps + 1) {
+        tc_fence_after();
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+// Tiles over the columns, as make_plan, for tiles of 256 rows over `pairs`
+// pairs of SMs, in groups of 32 columns (a group has one tile scale, and the
+// pair's MMA takes N in steps of 32).
+PairPlan make_pair_plan(int M, int N, int K, bool gated, bool row_scales, int pairs) {
+    PairPlan p{};
+    p.tiles_m = (M + 2 * kBM - 1) / (2 * kBM);
+    p.groups = (N + 31) / 32;
+    p.num_kb = (K + kBlockK - 1) / kBlockK;
+    const int per_group = gated ? 64 : 32;
+    const int max_groups = kPairBufCols / per_group;
+    const int least = (p.groups + max_groups - 1) / max_groups;
+    const int most = p.groups < least + pairs ? p.groups : least + pairs;
+    long long best = -1;
+    int widest = 0;
+    for (int tn = least; tn <= most; ++tn) {
+        const int cols = (p.groups + tn - 1) / tn * per_group;
+        const long long waves = (static_cast<long long>(p.tiles_m) * tn + pairs - 1) / pairs;
+        const long long cost = waves * (cols + 64);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.tiles_n = tn;
+            widest = cols;
+        }
+    }
+    p.half_rows = widest / 2;
+    p.s_cols = row_scales ? widest : 0;
+    return p;
+}
+
+std::atomic<unsigned> g_pair_attr_set_mask[3];
+
+template <int kMode>
+cudaError_t launch_pair(const void *A, const float *As, const void *B0, const float *Bs0,
+                        const void *B1, const float *Bs1, const Out &out, int M, int N, int K,
+                        const DeviceInfo &dev, cudaStream_t stream) {
+    auto kernel = swiglu_gemm_b128_pair_kernel<kMode>;
+    const unsigned bit = 1u << (dev.device & 31);
+    if (!(g_pair_attr_set_mask[kMode].load() & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(PairLayout<kMode>::kSmem));
+        if (e != cudaSuccess) return e;
+        // the register split needs the whole launch's registers
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+        g_pair_attr_set_mask[kMode].fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = PairLayout<kMode>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2);
+    int max_clusters = 0;
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&max_clusters, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (max_clusters < 1) return cudaErrorInvalidConfiguration;
+    const PairPlan p = make_pair_plan(M, N, K, kMode == kGated, kMode == kRowScales, max_clusters);
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapSwizzle none = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const uint64_t k64 = static_cast<uint64_t>(K), n64 = static_cast<uint64_t>(N);
+    const uint32_t half = static_cast<uint32_t>(p.half_rows);
+    CUtensorMap ta, tas, tb, tu, tbs;
+    if (!encode_tmap_2d(&ta, A, u8, k64, M, k64, kBlockK, kBM, sw) ||
+        !encode_tmap_2d(&tas, As, f32, M, p.num_kb, static_cast<uint64_t>((M + 3) / 4 * 4) * 4, 128,
+                        kSlotBlocks, none) ||
+        !encode_tmap_2d(&tb, B0, u8, k64, n64, k64, kBlockK, half, sw))
+        return cudaErrorInvalidValue;
+    tu = tb;
+    tbs = tas;
+    if (kMode == kGated && !encode_tmap_2d(&tu, B1, u8, k64, n64, k64, kBlockK, half, sw))
+        return cudaErrorInvalidValue;
+    if (kMode == kRowScales &&
+        !encode_tmap_2d(&tbs, Bs0, f32, n64, p.num_kb, n64 * 4, static_cast<uint32_t>(p.s_cols),
+                        kSlotBlocks, none))
+        return cudaErrorInvalidValue;
+    const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+    const long long pairs = tiles < max_clusters ? tiles : max_clusters;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    e = cudaLaunchKernelEx(&cfg, kernel, ta, tas, tb, tu, tbs, Bs0, Bs1, out, M, N, p);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
 // Tiles over the columns and the ring.  A tile costs its columns plus a
 // constant (its rows of A are loaded and read whatever its width), and the
 // tiles of all rows run in waves over the SMs: the cheapest count wins.
@@ -586,6 +1204,7 @@ template <int kMode>
 cudaError_t launch(const void *A, const float *As, const void *B0, const float *Bs0, const void *B1,
                    const float *Bs1, const Out &out, int M, int N, int K, const DeviceInfo &dev,
                    cudaStream_t stream) {
+    if (M > kBM) return launch_pair<kMode>(A, As, B0, Bs0, B1, Bs1, out, M, N, K, dev, stream);
     const Plan p = make_plan(M, N, K, kMode == kGated, kMode == kRowScales, dev.sm_count);
     if (p.smem > kMaxSmem || p.bufs < 2) return cudaErrorInvalidValue;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
