@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "gemm_common.cuh"
@@ -54,8 +55,8 @@ constexpr int kBlockK = 128;                 // bytes = e4m3 values per block an
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 4);  // (register shares go by groups of 4 warps)
 // 384 threads start with 168 registers each; the accumulating warps take
-// what the third group of warps gives back: 256 * 232 + 128 * 40 = 384 * 168.
-constexpr int kRegsLaunch = 168, kRegsEpi = 232, kRegsRest = 40;
+// what the third group of warps gives back: 256 * 224 + 128 * 56 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsEpi = 224, kRegsRest = 56;
 static_assert(256 * kRegsEpi + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
 constexpr int kMaxUnits = 32;                // units of 8 columns per tile
 constexpr int kMaxStages = 24;
@@ -280,20 +281,6 @@ __device__ __forceinline__ void store_tile(const unsigned long long (&acc)[4][16
             }
         }
     }
-}
-
-// Tile scales.  A tile's columns span at most three blocks of 128 (gated: two
-// of each weight); per block of the reduction the slot holds, behind the 128
-// row scales, four values: plain, of blocks b0 .. b0 + 3 (the last one
-// repeated), gated, of blocks b0, b0 + 1 of Wg and of Wu.  The scales' warp
-// fetches them ahead of the copies' pace (lanes 0..3, one table row each).
-template <int kMode>
-__device__ __forceinline__ const float *tile_scale_source(const float *bs0, const float *bs1, int b0,
-                                                          int lane, int N, int num_kb) {
-    const int blocks = (N + 127) / 128;
-    const int i = kMode == kGated ? (lane & 1) : (lane & 3);
-    const float *table = (kMode == kGated && (lane & 2)) ? bs1 : bs0;
-    return table + static_cast<int64_t>(min(b0 + i, blocks - 1)) * num_kb;
 }
 
 // tm_b*: rows of B (gated: of Wg and Wu), boxes of 8 q (lo) and 8 (q + 1)
@@ -677,23 +664,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 // issue its copies (B; A; the scales), one copy per block each, since one
 // thread issuing all of them took longer than a block's MMAs.
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 4;
 constexpr int kSlotBlocks = 4;    // blocks of the reduction per slot of scales
 constexpr int kPairBufCols = 256;
 constexpr uint32_t kPairStageBytes = 32 * 1024;
 constexpr int kPairMaxSlots = 4;
 constexpr uint32_t kPairBars = 2 * kPairStages + 2 * kPairMaxSlots + 2 * 2 + 1;
 
+// Output staging of a warp: 32 rows by 32 columns leave by one TMA store, so
+// the warp goes on to its next tile while they drain.
+constexpr uint32_t kOutBytes = 8192;   // four such boxes of bf16, two of fp32
+
 template <int kMode>
 struct PairLayout {
-    // per slot: row scales of A [4][128], then of B [4][s_cols], or the tile
-    // scales [4][4]
+    // per slot: row scales of A [4][128], then of B [4][s_cols], or tile
+    // scales [4][half of the tile][group of the half]
     static constexpr int kSlots = kMode == kRowScales ? 2 : 4;
     static constexpr uint32_t kOffB = kSlotBlocks * 512;
     static constexpr uint32_t kSlotBytes = kOffB + kSlotBlocks * (kMode == kRowScales ? 1024 : 32);
-    static constexpr uint32_t kOffSlots = kPairStages * kPairStageBytes;
-    static constexpr uint32_t kOffOut = kOffSlots + kSlots * kSlotBytes;
-    static constexpr uint32_t kOffBar = kOffOut + kEpiWarps * kStageOutBytes;
+    static constexpr uint32_t kOffOut = kPairStages * kPairStageBytes;
+    static constexpr uint32_t kOffSlots = kOffOut + kEpiWarps * kOutBytes;
+    static constexpr uint32_t kOffBar = kOffSlots + kSlots * kSlotBytes;
     static constexpr uint32_t kSmem = kOffBar + 8 * kPairBars + 32 + 1024;
     static_assert(kSmem <= kMaxSmem, "exceeds the 227 KB opt-in shared memory");
 };
@@ -718,6 +709,18 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// Arrive on the barrier at this offset of both CTAs' shared memory when every
+// MMA issued so far by this thread has completed (one commit for the pair:
+// B200, M = 8192 N = 4096 K = 14336, the MMAs alone: 2.5 PFLOP/s with a commit
+// per CTA, PLACEHOLDER with this).
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 // tm_b: rows of B (gated: of Wg), tm_u: of Wu, boxes of half_rows rows.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -726,6 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  const __grid_constant__ CUtensorMap tm_b,
                                  const __grid_constant__ CUtensorMap tm_u,
                                  const __grid_constant__ CUtensorMap tm_bs,
+                                 const __grid_constant__ CUtensorMap tm_y,
+                                 const __grid_constant__ CUtensorMap tm_yg,
+                                 const __grid_constant__ CUtensorMap tm_yu,
                                  const float *__restrict__ bs0, const float *__restrict__ bs1,
                                  const Out out, int M, int N, const PairPlan p) {
     using L = PairLayout<kMode>;
@@ -771,8 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_as);
-        tma_prefetch_desc(kMode == kGated && rank == 1 ? &tm_u : &tm_b);
+        // (tm_u is left to its first use: naming it here by rank made the
+        // compiler keep the loop's uniform values in spilled registers)
+        tma_prefetch_desc(&tm_b);
         if (kMode == kRowScales) tma_prefetch_desc(&tm_bs);
+        tma_prefetch_desc(&tm_y);
     }
     if (warp == kEpiWarps + 1) {
         tmem_alloc_pair(smem_u32(tmem_ptr), kTmemCols);
@@ -842,12 +851,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
                 int m0, g0, cnt;
                 tile_of(t, m0, g0, cnt);
+                // tile scales: lane = (block, half of the tile, group of the
+                // half), the value its accumulating warps multiply by
                 const float *src = nullptr;
-                if (kMode != kRowScales && lane < 16)  // lane: block lane / 4 of the slot, value lane % 4
-                    src = tile_scale_source<kMode>(bs0, bs1, g0 / 4, lane & 3, N, num_kb);
+                if (kMode != kRowScales) {
+                    const int j = lane & 3;
+                    const int group = g0 + ((lane & 4) ? (cnt + 1) / 2 : 0) + (kMode == kGated ? (j & 1) : j);
+                    const float *table = (kMode == kGated && (j & 2)) ? bs1 : bs0;
+                    src = table + static_cast<int64_t>(min(group / 4, (N + 127) / 128 - 1)) * num_kb;
+                }
                 for (int kb = 0; kb < num_kb; kb += kSlotBlocks) {
                     float v = 0.0f;
-                    if (kMode != kRowScales && lane < 16) v = __ldg(src + min(kb + lane / 4, num_kb - 1));
+                    if (kMode != kRowScales) v = __ldg(src + min(kb + lane / 8, num_kb - 1));
                     if (!mbar_wait_long(bar_sempty + 8 * slot, phase ^ 1u, abort_flag)) {
                         failed = true;
                         break;
@@ -855,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t sb = bar_sfull + 8 * slot;
                     const uint32_t dst = base + L::kOffSlots + slot * L::kSlotBytes;
                     if (kMode != kRowScales) {
-                        if (lane < 16) sts_f32(dst + L::kOffB + 4u * lane, v);
+                        sts_f32(dst + L::kOffB + 4u * lane, v);
                         __syncwarp();
                     }
                     if (lane == 0) {
@@ -879,8 +894,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {
             // ------------------------------------------ MMA issuer (pair)
             const uint32_t idesc = make_idesc(0u, 2 * kBM, static_cast<uint32_t>(2 * p.half_rows));
-            const uint32_t empty_r1 = map_to_rank(bar_empty, 1);
-            const uint32_t tfull_r1 = map_to_rank(bar_tfull, 1);
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
@@ -897,10 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8_pair(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
-                    mma_commit_pair(bar_empty + 8 * stage);
-                    mma_commit_pair(empty_r1 + 8 * stage);
-                    mma_commit_pair(bar_tfull + 8 * buf);
-                    mma_commit_pair(tfull_r1 + 8 * buf);
+                    mma_commit_both(bar_empty + 8 * stage);
+                    mma_commit_both(bar_tfull + 8 * buf);
                     if (++stage == kPairStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -920,9 +931,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t obuf = base + L::kOffOut + static_cast<uint32_t>(warp) * kStageOutBytes;
+        const uint32_t obuf = base + L::kOffOut + static_cast<uint32_t>(warp) * kOutBytes;
+        int onext = 0;  // next staging box
         const uint32_t tempty_r0 = map_to_rank(bar_tempty, 0);
-        int slot = 0, buf = 0;
+        int slot = 0;
+        uint32_t buf8 = 0;            // 8 x the TMEM buffer in turn
+        uint32_t pa = 0, pb = 0;      // the next block's scales of A (this row's) and of B
         uint32_t sphase = 0, bphase = 0;
         for (int t = pair; t < num_tiles && !failed; t += num_pairs) {
             int m0, g0, cnt;
@@ -934,72 +948,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(32, M - m0 - 32 * quad);  // <= 0: none
             const uint32_t col0 = 32u * static_cast<uint32_t>(first);
             const uint32_t col2 = kMode == kGated ? col0 + static_cast<uint32_t>(p.half_rows) : col0 + 64u;
-            // groups are read in pairs, in this order: plain 0 1 2 3, gated 0 2
-            // 1 3 (an odd count reads one more, whose sums are not stored)
-            const int groups = rows <= 0 ? 0 : (kMode == kGated ? 2 * mine : (mine + 1) / 2 * 2);
-            constexpr int kOrder[4] = {0, kMode == kGated ? 2 : 1, kMode == kGated ? 1 : 2, 3};
+            // groups are read in pairs (an odd count reads one more, gated always
+            // all four; sums of columns beyond the tile are not stored)
+            const int groups = rows <= 0 || mine == 0 ? 0 : (kMode == kGated ? 4 : (mine + 1) / 2 * 2);
             unsigned long long acc[4][16];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
-            // each group's tile scale within its block's four
-            uint32_t at[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                at[j] = 4u * static_cast<uint32_t>((g0 + first + (kMode == kGated ? (j & 1) : j)) / 4 - g0 / 4 +
-                                                   (kMode == kGated ? (j & 2) : 0));
-
             float sa = 0.0f, sb[4] = {};
             uint32_t srow = 0;        // this block's row scales of B
             uint32_t v[2][32];
             // One block ahead: wait for its accumulators, start reading them,
             // and fetch its scales.
-            auto open_block = [&](int kb) -> bool {
-                if (kb % kSlotBlocks == 0 && !mbar_wait_long(bar_sfull + 8 * slot, sphase, abort_flag)) return false;
-                if (!mbar_wait_long(bar_tfull + 8 * buf, bphase, abort_flag)) return false;
+            auto open_block = [&](bool new_slot) -> bool {
+                if (new_slot) {
+                    if (!mbar_wait_long(bar_sfull + 8 * slot, sphase, abort_flag)) return false;
+                    pa = base + L::kOffSlots + slot * L::kSlotBytes + 4u * (quad * 32 + lane);
+                    pb = base + L::kOffSlots + slot * L::kSlotBytes + L::kOffB + (kMode == kRowScales ? 0u : 16u * half);
+                }
+                if (!mbar_wait_long(bar_tfull + buf8, bphase, abort_flag)) return false;
                 tc_fence_after();
                 if (groups == 0) return true;
-                tmem_ld_32x32b_x32(lanes + static_cast<uint32_t>(buf * kPairBufCols) + col0, v[0]);
-                const uint32_t src = base + L::kOffSlots + slot * L::kSlotBytes;
-                const uint32_t blk = static_cast<uint32_t>(kb % kSlotBlocks);
-                sa = lds_f32(src + blk * 512u + 4u * (quad * 32 + lane));
+                tmem_ld_32x32b_x32(lanes + 32u * buf8 + col0, v[0]);
+                sa = lds_f32(pa);
+                pa += 512u;
                 if constexpr (kMode != kRowScales) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sb[j] = lds_f32(src + L::kOffB + blk * 16u + at[j]);
+                    const uint4 w = lds_v4(pb);
+                    pb += 32u;
+                    sb[0] = __uint_as_float(w.x);
+                    sb[1] = __uint_as_float(w.y);
+                    sb[2] = __uint_as_float(w.z);
+                    sb[3] = __uint_as_float(w.w);
                 } else {
-                    srow = src + L::kOffB + blk * 4u * static_cast<uint32_t>(p.s_cols);
+                    srow = pb;
+                    pb += 4u * static_cast<uint32_t>(p.s_cols);
                 }
                 return true;
             };
-            if (!open_block(0)) {
+            if (!open_block(true)) {
                 failed = true;
                 break;
             }
             for (int kb = 0; kb < num_kb; ++kb) {
-                const uint32_t d = lanes + static_cast<uint32_t>(buf * kPairBufCols);
+                const uint32_t d = lanes + 32u * buf8;
                 float s[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[j] = sa * sb[j];
                 const float sa_now = sa;
                 const uint32_t srow_now = srow;
                 auto read = [&](int o) {
-                    const int g = kOrder[o];
-                    tmem_ld_32x32b_x32(d + (g < 2 ? col0 : col2) + 32u * (g & 1), v[o & 1]);
+                    tmem_ld_32x32b_x32(d + (o < 2 ? col0 : col2) + 32u * (o & 1), v[o & 1]);
                 };
                 auto add = [&](int o) {
-                    const int g = kOrder[o];
                     if constexpr (kMode == kRowScales)
-                        add_rows(acc[g], v[o & 1], sa_now, srow_now + 4u * ((g < 2 ? col0 : col2) + 32u * (g & 1)));
+                        add_rows(acc[o], v[o & 1], sa_now, srow_now + 4u * ((o < 2 ? col0 : col2) + 32u * (o & 1)));
                     else
-                        add_block(acc[g], v[o & 1], s[g]);
+                        add_block(acc[o], v[o & 1], s[o]);
                 };
                 // the next 32 columns are on their way while these are added
                 if (groups > 0) {
                     tmem_ld_wait(v[0]);
                     read(1);
                     add(0);
-                    if (groups > 2) {
+                    if (kMode == kGated || groups > 2) {
                         tmem_ld_wait(v[1]);
                         read(2);
                         add(1);
@@ -1012,34 +1024,103 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every value of this buffer has been read
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(tempty_r0 + 8 * buf);
-                if (++buf == 2) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
-                const bool slot_done = kb % kSlotBlocks == kSlotBlocks - 1 || kb + 1 == num_kb;
+                if (lane == 0) mbar_arrive_remote(tempty_r0 + buf8);
+                buf8 ^= 8u;
+                if (buf8 == 0) bphase ^= 1u;
+                const bool last = kb + 1 == num_kb;
+                const bool slot_done = (kb & (kSlotBlocks - 1)) == kSlotBlocks - 1 || last;
                 const uint32_t slot_bar = bar_sempty + 8 * slot;
                 if (slot_done && ++slot == L::kSlots) {
                     slot = 0;
                     sphase ^= 1u;
                 }
-                if (kb + 1 < num_kb && !open_block(kb + 1)) {
+                if (!last && !open_block(slot_done)) {
                     failed = true;
                     break;
                 }
                 if (groups > 2) add(3);
-                else if (groups > 0) add(1);
+                else if (kMode != kGated && groups > 0) add(1);
                 if (slot_done) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(slot_bar);
                 }
             }
             if (failed || groups == 0) continue;
-            // (units of 8 columns: the last group may reach past N)
-            const int64_t colg = 32 * (static_cast<int64_t>(g0) + first);
-            const int left = static_cast<int>((N - colg) / 8);
-            store_tile<kMode>(acc, out, obuf, lane, m0 + 32 * quad, colg, N, rows, min(4 * mine, left));
+            const int x0 = 32 * (g0 + first), y0 = m0 + 32 * quad;
+            // lane = row writes its 64 (bf16) or 128 bytes (fp32) where the
+            // TMA swizzle expects them; stores clip at N and M
+            auto put_bf16 = [&](const CUtensorMap &map, int group, auto value) {
+                const uint32_t box = obuf + static_cast<uint32_t>(onext) * 2048u;
+                if (lane == 0) bulk_wait_read<3>();  // the store from this box four boxes ago
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    sts_v4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
+                           make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3)));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&map, box, x0 + 32 * group, y0);
+                    bulk_commit();
+                }
+                onext = (onext + 1) & 3;
+            };
+            if constexpr (kMode == kGated) {
+                // (one copy of the code per activation: deciding inside, value
+                // by value, cost the loop above its uniform registers)
+                auto put_gated = [&](auto which) {
+                    constexpr int kAct = decltype(which)::value;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (j < mine)
+                            put_bf16(tm_y, j, [&](int i) {
+                                return pack_bf16x2(
+                                    act::gated<false>(kAct, out.alpha, lo2(acc[j][i]), lo2(acc[2 + j][i])),
+                                    act::gated<false>(kAct, out.alpha, hi2(acc[j][i]), hi2(acc[2 + j][i])));
+                            });
+                };
+                if (out.act == act::kSilu) put_gated(std::integral_constant<int, act::kSilu>());
+                else put_gated(std::integral_constant<int, act::kGeluTanh>());
+                if (out.g) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (j < mine) {
+                            put_bf16(tm_yg, j, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+                            put_bf16(tm_yu, j, [&](int i) { return pack_bf16x2(lo2(acc[2 + j][i]), hi2(acc[2 + j][i])); });
+                        }
+                    }
+                }
+            } else if (!out.f32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < mine)
+                        put_bf16(tm_y, j, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j < mine) {
+                        const uint32_t box = obuf + static_cast<uint32_t>(onext & 1) * 4096u;
+                        if (lane == 0) bulk_wait_read<1>();  // the store from this box two boxes ago
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const unsigned long long a0 = acc[j][2 * c], a1 = acc[j][2 * c + 1];
+                            sts_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4),
+                                   make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
+                                              static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32)));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tm_y, box, x0 + 32 * j, y0);
+                            bulk_commit();
+                        }
+                        onext = (onext + 1) & 3;
+                    }
+                }
+            }
         }
+        if (lane == 0) bulk_wait<0>();
     }
 
     if (failed) atomicOr(&g_gemm_b128_status, 1u);
@@ -1127,7 +1208,7 @@ cudaError_t launch_pair(const void *A, const float *As, const void *B0, const fl
     const CUtensorMapSwizzle none = CU_TENSOR_MAP_SWIZZLE_NONE;
     const uint64_t k64 = static_cast<uint64_t>(K), n64 = static_cast<uint64_t>(N);
     const uint32_t half = static_cast<uint32_t>(p.half_rows);
-    CUtensorMap ta, tas, tb, tu, tbs;
+    CUtensorMap ta, tas, tb, tu, tbs, ty, tyg, tyu;
     if (!encode_tmap_2d(&ta, A, u8, k64, M, k64, kBlockK, kBM, sw) ||
         !encode_tmap_2d(&tas, As, f32, M, p.num_kb, static_cast<uint64_t>((M + 3) / 4 * 4) * 4, 128,
                         kSlotBlocks, none) ||
@@ -1141,10 +1222,20 @@ cudaError_t launch_pair(const void *A, const float *As, const void *B0, const fl
         !encode_tmap_2d(&tbs, Bs0, f32, n64, p.num_kb, n64 * 4, static_cast<uint32_t>(p.s_cols),
                         kSlotBlocks, none))
         return cudaErrorInvalidValue;
+    const bool ok = out.f32 ? encode_tmap_2d(&ty, out.y, f32, n64, M, n64 * 4, 32, 32, sw)
+                            : encode_tmap_2d(&ty, out.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n64, M, n64 * 2, 32,
+                                             32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok) return cudaErrorInvalidValue;
+    tyg = tyu = ty;
+    if (out.g && (!encode_tmap_2d(&tyg, out.g, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n64, M, n64 * 2, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B) ||
+                  !encode_tmap_2d(&tyu, out.u, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n64, M, n64 * 2, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_64B)))
+        return cudaErrorInvalidValue;
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
     const long long pairs = tiles < max_clusters ? tiles : max_clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    e = cudaLaunchKernelEx(&cfg, kernel, ta, tas, tb, tu, tbs, Bs0, Bs1, out, M, N, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, ta, tas, tb, tu, tbs, ty, tyg, tyu, Bs0, Bs1, out, M, N, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
