@@ -18,9 +18,12 @@ NULL, DIM, MDIM, MPTR, DTYPE, OVER, EPI, BLOCK = (
 
 
 def test_product_plans_keep_memory_bounds():
-    """Shared memory, TMA boxes, TMEM columns and unit counts of the
-    block-scaled products' plans (gemm_b128_plan_check.cu)."""
-    _build_and_run(["tests/gemm_b128_plan_check.cu", "up_projection_b200/csrc/tmap.cu"], 100000)
+    """Shared memory, TMA boxes, TMEM columns and tiles of the block-scaled
+    products' plans, M > 128 and M <= 128 (gemm_b128_plan_check.cu,
+    gemm_b128_stream_plan_check.cu)."""
+    csrc = "up_projection_b200/csrc/"
+    _build_and_run(["tests/gemm_b128_plan_check.cu", csrc + "gemm_b128_stream.cu", csrc + "tmap.cu"], 100000)
+    _build_and_run(["tests/gemm_b128_stream_plan_check.cu", csrc + "tmap.cu"], 100000)
 
 
 # swiglu_quant_b128(X, Q, S, R, C, dtype, block, transpose)

@@ -148,7 +148,8 @@ def test_gemm_matches_fp64(M, N, K, block, out):
 
 
 @pytest.mark.parametrize("block", ["tile", "row"])
-@pytest.mark.parametrize("M,N,K", SHAPES + [(200, 14336, 384), (40, 6912, 1536)])
+@pytest.mark.parametrize("M,N,K", SHAPES + [(200, 14336, 384), (40, 6912, 1536), (8, 4096, 4096), (20, 512, 8192), (1, 8, 4112),
+                                            (33, 40000, 256), (2, 60000, 144), (70, 24000, 272)])
 def test_gemm_integers_are_exact(M, N, K, block):
     """Small integers and power-of-two scales: every partial sum is exact in
     fp32, so the fp32 result has to be equal, bit for bit, and every scale has
@@ -201,6 +202,28 @@ def test_gated_matches_fp64(M, N, K, act, alpha, gu):
     if gu:
         within(r[1], G, 2.0 ** -8 * G.abs() + 1.01 * c * AG, "G")
         within(r[2], U, 2.0 ** -8 * U.abs() + 1.01 * c * AU, "U")
+
+
+@pytest.mark.parametrize("M", [1, 8, 20, 60, 128, 300])
+@pytest.mark.parametrize("K", [384, 400])
+@pytest.mark.parametrize("order", ["gate first", "up first", "one weight"])
+def test_gated_weights_in_any_place(M, K, order):
+    """The two weights behind one another in either order, or the same one:
+    integer operands, so G and U are exact before their rounding."""
+    N = 520
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + K)
+    codes = torch.tensor([0.0, 1.0, 2.0, -1.0, -2.0], device=dev()).to(torch.float8_e4m3fn).view(torch.uint8)
+    A = codes[torch.randint(0, 5, (M, K), generator=g, device="cuda")]
+    W = codes[torch.randint(0, 5, (2, N, K), generator=g, device="cuda")]
+    kb = (K + 127) // 128
+    s = [torch.exp2(torch.randint(-2, 3, ((N + 127) // 128, kb), generator=g, device="cuda").float()) for _ in range(2)]
+    As = ref.row_scales(torch.exp2(torch.randint(-2, 3, (M, kb), generator=g, device="cuda").float()))
+    i, j = {"gate first": (0, 1), "up first": (1, 0), "one weight": (0, 0)}[order]
+    H, G, U = up.swiglu_fwd_b128(A, As, W[i], s[0], W[j], s[1], return_gu=True)
+    synced()
+    assert torch.equal(G, ref.product(A, As, W[i], s[0], "tile")[0].to(torch.bfloat16))
+    assert torch.equal(U, ref.product(A, As, W[j], s[1], "tile")[0].to(torch.bfloat16))
 
 
 def test_products_write_inside_their_outputs():

@@ -1,0 +1,265 @@
+// b128.cuh -- pieces shared by the two kernels of the block-scaled e4m3
+// products (gemm_b128.cu: large M; gemm_b128_stream.cu: M <= 128).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "activation.cuh"
+#include "gemm_common.cuh"
+#include "ptx.cuh"
+
+namespace swiglu {
+namespace b128 {
+
+using namespace dev;
+using gemm::mbar_wait_drain;
+
+constexpr int kBM = 128;                     // rows of A per CTA
+constexpr int kBlockK = 128;                 // bytes = e4m3 values per block and stage row
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 4);  // (register shares go by groups of 4 warps)
+// 384 threads start with 168 registers each; the accumulating warps take
+// what the third group of warps gives back: 256 * 224 + 128 * 56 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsEpi = 224, kRegsRest = 56;
+static_assert(256 * kRegsEpi + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+constexpr int kTmemCols = 512;
+constexpr uint32_t kMaxSmem = 227 * 1024;
+
+enum : int { kTileScales = 0, kRowScales = 1, kGated = 2 };
+
+struct Out {
+    void *y;                 // Y or H
+    __nv_bfloat16 *g, *u;    // gated: null or the two products
+    int f32;
+    int act;
+    float alpha;
+};
+
+__device__ __forceinline__ void griddep_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void griddep_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// mbar_wait for waits that are long by design: after one test the thread
+// sleeps until the phase completes (or 20 us have passed) instead of polling,
+// which leaves the issue slots to the accumulating warps.
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// The MMAs and commits below are called by a whole converged warp and issued by
+// the thread that elect.sync names (the same one each time): with the loop's
+// values uniform over the warp the compiler keeps descriptors in uniform
+// registers.  (B200, one CTA, chains of four MMAs with M = 128: 39 cycles each
+// at N = 16, 128 at N = 256; issued under `lane == 0` 51 at best and, with a
+// few address computations between them, up to 160 -- more than the MMA.)
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+        : "memory");
+}
+
+// acc += s * d on a pair of columns.
+__device__ __forceinline__ void fma2(unsigned long long &acc, uint32_t d0, uint32_t d1,
+                                     unsigned long long s) {
+    asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(d0), "r"(d1), "l"(s));
+}
+
+__device__ __forceinline__ unsigned long long pair2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float lo2(unsigned long long v) {
+    return __uint_as_float(static_cast<uint32_t>(v));
+}
+__device__ __forceinline__ float hi2(unsigned long long v) {
+    return __uint_as_float(static_cast<uint32_t>(v >> 32));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// A warp's 32 rows x 64 bytes to global memory through its staging buffer:
+// lane = row writes its four 16-byte chunks (swizzled over the banks), then
+// every four lanes store 64 consecutive bytes of a row.  `cols16` of the four
+// chunks belong to the tile.
+__device__ __forceinline__ void store_rows(uint32_t buf, int lane, const uint4 (&v)[4], char *dst,
+                                           int64_t row_bytes, int rows, int cols16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts_v4(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), v[j]);
+    __syncwarp();
+    const int j = lane & 3;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + (lane >> 2);
+        const uint4 w = lds_v4(buf + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+        if (r < rows && j < cols16) *reinterpret_cast<uint4 *>(dst + r * row_bytes + j * 16) = w;
+    }
+    __syncwarp();
+}
+
+// One block's 32 accumulator columns of a warp, times their scales, into the
+// running sums.  Tile scales: the four units of 8 columns take slo below
+// unit `cut` (counted from these columns) and shi from there on.
+__device__ __forceinline__ void add_tile(unsigned long long (&acc)[16], const uint32_t (&v)[32],
+                                         float slo, float shi, int cut) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float s = u < cut ? slo : shi;
+        const unsigned long long s2 = pair2(s, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma2(acc[4 * u + i], v[8 * u + 2 * i], v[8 * u + 2 * i + 1], s2);
+    }
+}
+
+// The same with one scale for all 32 columns.
+__device__ __forceinline__ void add_block(unsigned long long (&acc)[16], const uint32_t (&v)[32], float s) {
+    const unsigned long long s2 = pair2(s, s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) fma2(acc[i], v[2 * i], v[2 * i + 1], s2);
+}
+
+// Row scales: one per column, in shared memory at sb.
+__device__ __forceinline__ void add_rows(unsigned long long (&acc)[16], const uint32_t (&v)[32],
+                                         float sa, uint32_t sb) {
+    const unsigned long long sa2 = pair2(sa, sa);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 w = lds_v4(sb + 16u * i);
+        const unsigned long long s0 = pair2(__uint_as_float(w.x), __uint_as_float(w.y));
+        const unsigned long long s1 = pair2(__uint_as_float(w.z), __uint_as_float(w.w));
+        fma2(acc[2 * i], v[4 * i], v[4 * i + 1], mul2(s0, sa2));
+        fma2(acc[2 * i + 1], v[4 * i + 2], v[4 * i + 3], mul2(s1, sa2));
+    }
+}
+
+// A warp's share of a tile, from its sums to global memory: rows row0 .. (at
+// most 32, `rows` of them), columns colg .. of `mine` units of 8.  acc[0..3]:
+// groups of 32 columns (gated: 0, 1 of G and 2, 3 of U).
+template <int kMode>
+__device__ __forceinline__ void store_tile(const unsigned long long (&acc)[4][16], const Out &out,
+                                           uint32_t buf, int lane, int64_t row0, int64_t colg, int N,
+                                           int rows, int mine) {
+    auto put_bf16 = [&](void *y, int group, int units_left, auto value) {
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[c] = make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3));
+        store_rows(buf, lane, v, static_cast<char *>(y) + 2 * (row0 * N + colg + 32 * group), 2ll * N,
+                   rows, units_left);
+    };
+    if constexpr (kMode == kGated) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int left = mine - 4 * j;
+            if (left > 0) {
+                put_bf16(out.y, j, left, [&](int i) {
+                    return pack_bf16x2(
+                        act::gated<false>(out.act, out.alpha, lo2(acc[j][i]), lo2(acc[2 + j][i])),
+                        act::gated<false>(out.act, out.alpha, hi2(acc[j][i]), hi2(acc[2 + j][i])));
+                });
+                if (out.g) {
+                    put_bf16(out.g, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+                    put_bf16(out.u, j, left,
+                             [&](int i) { return pack_bf16x2(lo2(acc[2 + j][i]), hi2(acc[2 + j][i])); });
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = mine - 4 * j;
+            if (left > 0) {
+                if (!out.f32) {
+                    put_bf16(out.y, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 16 columns = 64 bytes each
+                        uint4 v[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const unsigned long long a0 = acc[j][8 * h + 2 * c], a1 = acc[j][8 * h + 2 * c + 1];
+                            v[c] = make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
+                                              static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32));
+                        }
+                        store_rows(buf, lane, v,
+                                   static_cast<char *>(out.y) + 4 * (row0 * N + colg + 32 * j + 16 * h),
+                                   4ll * N, rows, 2 * (left - 2 * h));
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Opt in to the shared memory and check that the launch starts with the
+// registers its split hands out.
+template <typename Kernel>
+inline cudaError_t prepare_kernel(Kernel kernel, uint32_t smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa{};
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    return fa.numRegs < kRegsLaunch ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
+}  // namespace b128
+}  // namespace swiglu

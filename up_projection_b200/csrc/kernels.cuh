@@ -181,6 +181,15 @@ cudaError_t launch_gemm_b128(const void *A, const float *As, const void *B, cons
 cudaError_t launch_fwd_b128(const void *X, const float *Xs, const void *Wg, const float *Gs,
                             const void *Wu, const float *Us, void *H, int M, int N, int K,
                             const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream);
+// M <= 128 (gemm_b128_stream.cu), reached through the two above.
+constexpr int kB128StreamMaxM = 128;
+cudaError_t launch_gemm_b128_stream(const void *A, const float *As, const void *B, const float *Bs,
+                                    void *Y, int M, int N, int K, bool row_scales, int f32_out,
+                                    const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_fwd_b128_stream(const void *X, const float *Xs, const void *Wg, const float *Gs,
+                                   const void *Wu, const float *Us, void *H, int M, int N, int K,
+                                   const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t gemm_b128_stream_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream);
 cudaError_t gemm_b128_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream);
 
 // Tensor-map encoding through the driver entry point (no libcuda link).
