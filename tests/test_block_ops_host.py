@@ -26,6 +26,11 @@ def test_product_plans_keep_memory_bounds():
     _build_and_run(["tests/gemm_b128_stream_plan_check.cu", csrc + "tmap.cu"], 100000)
 
 
+def test_norm_ring_plans_keep_memory_bounds():
+    """Row rings, sums and items of the block norms (block_norm_plan_check.cu)."""
+    _build_and_run(["tests/block_norm_plan_check.cu"], 20000)
+
+
 # swiglu_quant_b128(X, Q, S, R, C, dtype, block, transpose)
 @pytest.mark.parametrize("args,code", [
     ((A[0], A[1], A[2], 4, 64, 2, 0, 0), DTYPE),

@@ -556,7 +556,10 @@ SWIGLU_API int swiglu_sync_status(cudaStream_t stream) {
     unsigned int w10 = 0;
     e = gemm_b128_stream_status_fetch_and_clear(&w10, stream);
     if (e != cudaSuccess) return from_cuda(e);
-    return (w1 | w2 | w3 | w4 | w5 | w6 | w7 | w8 | w9 | w10) ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
+    unsigned int w11 = 0;
+    e = block_norm_status_fetch_and_clear(&w11, stream);
+    if (e != cudaSuccess) return from_cuda(e);
+    return (w1 | w2 | w3 | w4 | w5 | w6 | w7 | w8 | w9 | w10 | w11) ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
 }
 
 SWIGLU_API int swiglu_selftest_wait_timeout(cudaStream_t stream) {

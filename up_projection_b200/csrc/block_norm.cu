@@ -18,16 +18,45 @@
 // All sums and statistics are fp32; each output is rounded once.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
+#include "b128.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
 namespace swiglu {
+
+// Status word of this translation unit's kernels (bit 0 = a wait gave up).
+__device__ unsigned int g_block_norm_status;
+
 namespace {
 
 using namespace dev;
+using b128::griddep_launch_dependents;
+using b128::griddep_wait;
 
 constexpr int kRowThreadsMax = 512;
 constexpr int kBlockThreads = 256;  // row groups fill a block up to this
+
+// Pairs of fp32 values: one instruction for two operations.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float lo2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
 template <bool kBf16>
 struct Vec {
@@ -43,6 +72,40 @@ struct Vec {
                 f[i] = __uint_as_float(w[i]);
             }
         }
+    }
+    // four consecutive elements
+    static __device__ __forceinline__ float4 load4(const uint4 *p, int64_t i) {
+        if constexpr (kBf16) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + i));
+            return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                               __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+        } else {
+            return __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i));
+        }
+    }
+    static __device__ __forceinline__ void store4(uint4 *p, int64_t i, const float4 &x) {
+        if constexpr (kBf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(p) + i) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        } else {
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i) = x;
+        }
+    }
+    static __device__ __forceinline__ void unpack2(const uint4 &v, f2 (&f)[kE / 2]) {
+        float x[kE];
+        unpack(v, x);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) f[i] = pack2(x[2 * i], x[2 * i + 1]);
+    }
+    static __device__ __forceinline__ uint4 pack_pairs(const f2 (&f)[kE / 2]) {
+        float x[kE];
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+            x[2 * i] = lo2(f[i]);
+            x[2 * i + 1] = hi2(f[i]);
+        }
+        return pack(x);
     }
     static __device__ __forceinline__ uint4 pack(const float (&f)[kE]) {
         uint32_t w[4];
@@ -63,12 +126,16 @@ __device__ __forceinline__ void row_barrier(int group, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
-// Sum of K values over the T = 32 * warps threads of a row group.  `slots`
+__device__ __forceinline__ void block_barrier(int threads) {
+    asm volatile("bar.sync 15, %0;" ::"r"(threads) : "memory");
+}
+
+// Sum of K values over the T = 32 * warps threads (tid) of a row group.  `slots`
 // is the group's shared memory, two sets of K * 16 floats used in turn, so
 // one barrier per reduction is enough: a set is rewritten only after the
 // barrier of the next reduction, which every reader of this one has reached.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float *slots, int &turn, int group,
+__device__ __forceinline__ void row_sum(float (&v)[K], float *slots, int &turn, int group, int tid,
                                         int threads) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -79,8 +146,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float *slots, int &turn, 
     if (warps == 1) return;
     float *s = slots + turn * (K * 16);
     turn ^= 1;
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) {
+    const int w = tid >> 5;
+    if ((tid & 31) == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k) s[k * 16 + w] = v[k];
     }
@@ -139,7 +206,7 @@ __global__ void __launch_bounds__(kRowThreadsMax) block_norm_kernel(const NormAr
 #pragma unroll
                 for (int i = 0; i < kE; ++i) s[0] = fmaf(f[i], f[i], s[0]);
             }
-            row_sum<1>(s, slots[grp], turn, grp, T);
+            row_sum<1>(s, slots[grp], turn, grp, tid, T);
             r1 = 1.0f / sqrtf(s[0] * inv_d + a.eps);
             if (a.rstd1 && tid == 0) a.rstd1[row] = r1;
         }
@@ -154,18 +221,18 @@ __global__ void __launch_bounds__(kRowThreadsMax) block_norm_kernel(const NormAr
             E::unpack(y[v], f);
             E::unpack(r[v], q);
             if (c < nvec) {
-                if (a.w1) {
-                    float w[kE];
-                    E::unpack(__ldg(a.w1 + c), w);
+                float w[kE];
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) f[i] *= w[i];
-                }
+                for (int i = 0; i < kE; ++i) w[i] = 1.0f;
+                if (a.w1) E::unpack(__ldg(a.w1 + c), w);
                 if (gate) {
                     float g[kE];
                     E::unpack(__ldg(gate + c), g);
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) f[i] *= g[i];
+                    for (int i = 0; i < kE; ++i) w[i] *= g[i];
                 }
+#pragma unroll
+                for (int i = 0; i < kE; ++i) f[i] *= w[i];
             }
 #pragma unroll
             for (int i = 0; i < kE; ++i) {
@@ -175,7 +242,7 @@ __global__ void __launch_bounds__(kRowThreadsMax) block_norm_kernel(const NormAr
             if (c < nvec) st_stream_v4(a.Rn + base + c, E::pack(rn[v]));
         }
         if (a.w2) {
-            row_sum<1>(s, slots[grp], turn, grp, T);
+            row_sum<1>(s, slots[grp], turn, grp, tid, T);
             const float r2 = 1.0f / sqrtf(s[0] * inv_d + a.eps);
             if (a.rstd2 && tid == 0) a.rstd2[row] = r2;
 #pragma unroll
@@ -193,182 +260,528 @@ __global__ void __launch_bounds__(kRowThreadsMax) block_norm_kernel(const NormAr
     }
 }
 
+// ----------------------------------------------------------- row rings
+// With many rows, rows arrive by bulk copies.  Each row group has a ring of
+// `stages` rows of its operands in shared memory, filled by its first thread:
+// the sums of a row end with a barrier of the group, after which the stage of
+// the row before it is free.  What is in flight then depends neither on
+// registers nor on where the groups stand between their loads, sums and
+// stores.
+
+constexpr int kMaxRing = 8;
+constexpr int kMaxGroups = 16;   // row groups of one warp; of more, at most 8
+constexpr int kRingThreads = 512;
+constexpr uint32_t kRingRoom = 220 * 1024;
+// A wait of the ring that gave up: no further copies are made, and those under
+// way end before the block does.
+__device__ __noinline__ void ring_abandon(uint32_t full, int stages, int stage, uint32_t phase) {
+    for (int i = 0; i < stages; ++i) {
+        int never = 0;
+        (void)mbar_wait(full + 8 * stage, phase, &never);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+// The forward over runs of consecutive rows, one run per block; W1 g and W2
+// stay in registers.  M = 8192, D = 4096, bf16: 50 us, 82 % of the measured
+// copy bandwidth (the two barriers of a row leave the rest).
+template <bool kBf16, int kV>
+__global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const NormArgs a, const int T, const int groups,
+                                                                          const int stages) {
+    using E = Vec<kBf16>;
+    constexpr int kE = E::kE, kP = kE / 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float slots[8][2 * 16];
+    __shared__ __align__(8) unsigned long long bars[kMaxGroups * kMaxRing];
+    __shared__ int abort_flag;
+    const int grp = threadIdx.x / T, tid = threadIdx.x - grp * T;
+    const int nvec = a.D / kE;
+    const uint32_t row_bytes = 16u * nvec;
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    // a stage: Y, R, each `pitch` bytes, of which the copies fill the first
+    // row_bytes; the rest is zero from here on
+    const uint32_t pitch = 16u * kV * T;
+    const uint32_t ring = smem_u32(smem) + grp * stages * 2u * pitch;
+    const uint32_t full = smem_u32(bars) + 8u * (grp * kMaxRing);
+    if (nvec < kV * T)
+        for (int i = tid; i < stages * 2 * kV * T; i += T) sts_v4(ring + 16u * i, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) abort_flag = 0;
+    __syncthreads();
+    const int64_t row0 = a.M * blockIdx.x / gridDim.x + grp, row1 = a.M * (blockIdx.x + 1) / gridDim.x;
+    auto copy_row = [&](int64_t row, int to) {
+        const uint32_t fb = full + 8 * to, st = ring + to * 2u * pitch;
+        mbar_arrive_expect_tx(fb, 2u * row_bytes);
+        bulk_load(st, a.Y + row * nvec, row_bytes, fb);
+        bulk_load(st + pitch, a.R + row * nvec, row_bytes, fb);
+    };
+    if (tid == 0)
+        for (int i = 0; i < stages && row0 + i * groups < row1; ++i) copy_row(row0 + i * groups, i);
+
+    int turn = 0, stage = 0;
+    uint32_t phase = 0;
+    bool failed = false;
+    f2 hold_g[kV][kP], hold_w[kV][kP];
+    auto fetch_g = [&](int v, const uint4 *gate, f2 (&o)[kP]) {
+        const int c = v * T + tid;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = pack2(1.0f, 1.0f);
+        if (c >= nvec) return;
+        if (a.w1) E::unpack2(__ldg(a.w1 + c), o);
+        if (gate) {
+            f2 f[kP];
+            E::unpack2(__ldg(gate + c), f);
+#pragma unroll
+            for (int i = 0; i < kP; ++i) o[i] = mul2(o[i], f[i]);
+        }
+    };
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        const int c = v * T + tid;
+        E::unpack2(a.w2 && c < nvec ? __ldg(a.w2 + c) : make_uint4(0, 0, 0, 0), hold_w[v]);
+    }
+    int64_t gate_end = row0;        // first row of the next gate row
+    const uint4 *gate = nullptr;
+    for (int64_t row = row0; row < row1; row += groups) {
+        if (row >= gate_end) {
+            const int64_t gr = row / a.rows_per_gate;
+            gate_end = (gr + 1) * a.rows_per_gate;
+            gate = a.gate ? a.gate + gr * nvec : nullptr;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) fetch_g(v, gate, hold_g[v]);
+        }
+        // (a wait that gave up is recorded; the rows that follow are worked
+        // on all the same, so that the group's barriers match)
+        if (!failed && !mbar_wait(full + 8 * stage, phase, &abort_flag)) {
+            failed = true;
+            if (tid == 0) ring_abandon(full, stages, stage, phase);
+        }
+        const uint32_t st = ring + stage * 2u * pitch + 16u * tid;
+        f2 y[kV][kP];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) E::unpack2(lds_v4(st + 16u * v * T), y[v]);
+        auto refill = [&]() {   // the whole group is done with the row before this one
+            const int64_t next = row + static_cast<int64_t>(stages - 1) * groups;
+            if (tid == 0 && row > row0 && next < row1 && !failed) copy_row(next, stage > 0 ? stage - 1 : stages - 1);
+        };
+        float r1 = 1.0f;
+        if (a.w1) {
+            f2 q = 0ull;
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+#pragma unroll
+                for (int i = 0; i < kP; ++i) q = fma2(y[v][i], y[v][i], q);
+            float s[1] = {lo2(q) + hi2(q)};
+            row_sum<1>(s, slots[grp & 7], turn, grp, tid, T);
+            r1 = 1.0f / sqrtf(s[0] * inv_d + a.eps);
+            if (a.rstd1 && tid == 0) a.rstd1[row] = r1;
+        } else if (!a.w2) {
+            if (T > 32) row_barrier(grp, T);
+            else __syncwarp();
+        }
+        const f2 sr1 = pack2(a.scale * r1, a.scale * r1);
+        uint4 *Rn = a.Rn + row * nvec + tid, *N = a.N + row * nvec + tid;
+        f2 q = 0ull;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            f2 r[kP];
+            E::unpack2(lds_v4(st + pitch + 16u * v * T), r);
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                y[v][i] = fma2(sr1, mul2(y[v][i], hold_g[v][i]), r[i]);
+                q = fma2(y[v][i], y[v][i], q);
+            }
+            if (v * T + tid < nvec) st_stream_v4(Rn + v * T, E::pack_pairs(y[v]));
+        }
+        if (a.w2) {
+            float s[1] = {lo2(q) + hi2(q)};
+            row_sum<1>(s, slots[grp & 7], turn, grp, tid, T);
+            const float r2 = 1.0f / sqrtf(s[0] * inv_d + a.eps);
+            if (a.rstd2 && tid == 0) a.rstd2[row] = r2;
+            refill();
+            const f2 r22 = pack2(r2, r2);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                f2 w[kP];
+#pragma unroll
+                for (int i = 0; i < kP; ++i) w[i] = mul2(hold_w[v][i], mul2(y[v][i], r22));
+                if (v * T + tid < nvec) st_stream_v4(N + v * T, E::pack_pairs(w));
+            }
+        } else {
+            refill();
+        }
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (failed) atomicOr(&g_block_norm_status, 1u);
+}
+
+// ------------------------------------------------------------- backward
+
 struct NormBwdArgs {
     const uint4 *dRn, *dN, *Y, *Rn;  // dRn null: zero; dN null with w2
     const float *rstd1, *rstd2;
     const uint4 *w1, *w2, *gate;
-    uint4 *dY, *dR, *dgate;          // dgate: written here when a gate row has one worker
-    float *acc2, *acc1, *accg;       // workspaces: [workers][D], [workers][D], [items][D]
+    uint4 *dY, *dR, *dgate;          // dgate: written here when a gate row has one item
+    float *acc2, *acc1, *accg;       // workspaces: [blocks][D], [blocks][D], [items][D]
     int64_t rows_per_gate;           // rows of one gate row (all of them without per-row gates)
-    int64_t groups;                  // gate rows (1 without)
-    int splits;                      // workers that share a gate row's rows
+    int64_t gates;                   // gate rows (1 without)
+    int splits;                      // blocks that share a gate row's rows
     int D;
+    int T, groups;                   // threads per row, rows at a time
+    int stages;                      // rows of a group's ring
     float scale;
 };
 
-// A worker is one row group (blockDim.x threads); worker w of W takes items
-// w, w + W, ...; item = (gate row, split): a run of consecutive rows that
-// share their gate row.  Its column sums stay in registers and leave once:
-// acc2 = sum dN n; acc1 = sum dX y, or with per-row gates sum s g dX y and
-// per item accg = sum dX y.
-template <bool kBf16, int kV, bool kGroups>
-__global__ void __launch_bounds__(kRowThreadsMax) block_norm_bwd_kernel(const NormBwdArgs a) {
+// Block b takes items b, b + grid, ...; item = (gate row, split): a run of
+// consecutive rows that share their gate row, `groups` of them at a time.
+// Column sums stay in registers and leave once per block: acc2 = sum dN n;
+// acc1 = sum dX y, or with gate rows sum s g dX y and, where a gate row has
+// more than one item, accg = the item's sum dX y.
+// What is kept between the two passes over a row: with 16 elements a thread or
+// fewer, e and the products of the weights (in registers); with more they are
+// formed again, because the column sums alone fill half the registers.
+// D = 4096, bf16: M = 16384 137 us with the join, 90 % of the measured copy
+// bandwidth; M = 2048 30 us, 52 % (14 rows per block: filling the rings and
+// the join, 5 us, are a third of it).  One CTA-wide loop over rows read
+// straight from memory took 234 and 45 us: its loads waited for its barriers.
+template <bool kBf16, int kV, bool kGates>
+__global__ void __launch_bounds__(kRingThreads, 1) block_norm_bwd_kernel(const NormBwdArgs a) {
     using E = Vec<kBf16>;
     constexpr int kE = E::kE;
+    constexpr bool kHold = kV * kE <= 16;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float slots[8][2 * 3 * 16];
-    const int T = blockDim.x, tid = threadIdx.x, grp = threadIdx.y;
+    __shared__ __align__(8) unsigned long long bars[kMaxGroups * kMaxRing];
+    __shared__ int abort_flag;
+    const int T = a.T, groups = a.groups, stages = a.stages;
+    const int grp = threadIdx.x / T, tid = threadIdx.x - grp * T;
     const int nvec = a.D / kE;
+    const uint32_t row_bytes = 16u * nvec;
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    int turn = 0;
-    const int64_t workers = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    const int64_t me = static_cast<int64_t>(blockIdx.x) * blockDim.y + grp;
-    const int64_t items = a.groups * a.splits;
+    // a stage: dRn, dN, Y, Rn, each `pitch` bytes, of which the copies fill
+    // the first row_bytes; what they never fill (the rest, and operands that
+    // are not there) is zero from here on
+    const uint32_t pitch = 16u * kV * T;
+    const uint32_t ring = smem_u32(smem) + grp * stages * 4u * pitch;
+    if (nvec < kV * T || !a.dRn || !a.w2)
+        for (int i = tid; i < stages * 4 * kV * T; i += T) sts_v4(ring + 16u * i, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
+    const uint32_t full = smem_u32(bars) + 8u * (grp * kMaxRing);
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) abort_flag = 0;
+    __syncthreads();
+    const int64_t items = a.gates * a.splits;
+    auto rows_of = [&](int64_t item, int64_t &row0, int64_t &row1) {
+        const int64_t gr = item / a.splits, sp = item - gr * a.splits;
+        row0 = gr * a.rows_per_gate + a.rows_per_gate * sp / a.splits;
+        row1 = gr * a.rows_per_gate + a.rows_per_gate * (sp + 1) / a.splits;
+    };
 
-    float s2[kV][kE], s1[kV][kE], sg[kV][kE];
+    auto copy_row = [&](int64_t row, int to) {
+        const uint32_t fb = full + 8 * to, st = ring + to * 4u * pitch;
+        mbar_arrive_expect_tx(fb, row_bytes * (1u + (a.dRn ? 1u : 0u) + (a.w2 ? 2u : 0u)));
+        const int64_t o = row * nvec;
+        if (a.dRn) bulk_load(st, a.dRn + o, row_bytes, fb);
+        if (a.w2) bulk_load(st + pitch, a.dN + o, row_bytes, fb);
+        bulk_load(st + 2 * pitch, a.Y + o, row_bytes, fb);
+        if (a.w2) bulk_load(st + 3 * pitch, a.Rn + o, row_bytes, fb);
+    };
+    // The group's first thread copies a ring ahead of the row it works on.
+    // Without gate rows a block has one item, and the row to copy follows from
+    // the row at hand; with them the copies go on into the block's next items.
+    int64_t next_item = blockIdx.x, next_row = 0, next_end = 0;
+    int put = 0;
+    auto copy_next = [&]() {
+        while (next_row >= next_end && next_item < items) {
+            rows_of(next_item, next_row, next_end);
+            next_row += grp;
+            next_item += gridDim.x;
+        }
+        if (next_row >= next_end) return;
+        copy_row(next_row, put);
+        if (++put == stages) put = 0;
+        next_row += groups;
+    };
+    if (tid == 0)
+        for (int i = 0; i < stages; ++i) copy_next();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool failed = false, first = true;
+
+    int turn = 0;
+    constexpr int kP = kE / 2;
+    // Column sums of this thread's rows: dN n, and dX y (with gate rows, those
+    // of the item at hand).  With gate rows sum1[D] gathers the block's
+    // sum s g dX y in shared memory, and shares[groups][D] is where the
+    // groups' dX y of an item meet.
+    f2 s2[kV][kP], sb[kV][kP];
+    float *sum1 = reinterpret_cast<float *>(smem + stages * groups * 4u * pitch), *shares = sum1 + a.D;
+    const float4 ones = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (kGates) {
+        for (int col = threadIdx.x; col < a.D; col += T * groups) sum1[col] = 0.0f;
+        block_barrier(T * groups);
+    }
 #pragma unroll
     for (int v = 0; v < kV; ++v)
 #pragma unroll
-        for (int i = 0; i < kE; ++i) s2[v][i] = s1[v][i] = sg[v][i] = 0.0f;
+        for (int i = 0; i < kP; ++i) s2[v][i] = sb[v][i] = 0ull;
 
-    for (int64_t item = me; item < items; item += workers) {
+    // s g W1 and W2 of vector v, from memory
+    auto fetch_g = [&](int v, const uint4 *gate, f2 (&o)[kP]) {
+        const int c = v * T + tid;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o[i] = pack2(a.scale, a.scale);
+        if (c >= nvec) return;
+        f2 f[kP];
+        if (a.w1) {
+            E::unpack2(__ldg(a.w1 + c), f);
+#pragma unroll
+            for (int i = 0; i < kP; ++i) o[i] = mul2(o[i], f[i]);
+        }
+        if (gate) {
+            E::unpack2(__ldg(gate + c), f);
+#pragma unroll
+            for (int i = 0; i < kP; ++i) o[i] = mul2(o[i], f[i]);
+        }
+    };
+    auto fetch_w = [&](int v) {
+        const int c = v * T + tid;
+        return a.w2 && c < nvec ? __ldg(a.w2 + c) : make_uint4(0, 0, 0, 0);
+    };
+    f2 hold_g[kHold ? kV : 1][kP];
+    f2 hold_w[kHold ? kV : 1][kP];
+
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        int64_t row0, row1;
+        rows_of(item, row0, row1);
         const int64_t gr = item / a.splits;
-        const int64_t sp = item - gr * a.splits;
-        const int64_t row0 = gr * a.rows_per_gate + a.rows_per_gate * sp / a.splits;
-        const int64_t row1 = gr * a.rows_per_gate + a.rows_per_gate * (sp + 1) / a.splits;
         const uint4 *gate = a.gate ? a.gate + gr * nvec : nullptr;
-        for (int64_t row = row0; row < row1; ++row) {
-            const int64_t base = row * nvec;
-            const float r1 = a.w1 ? a.rstd1[row] : 1.0f;
-            const float r2 = a.w2 ? a.rstd2[row] : 0.0f;
-            uint4 xd[kV], xn[kV], xy[kV], xr[kV];
+        if constexpr (kHold) {
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                const int c = v * T + tid;
-                xd[v] = xn[v] = xy[v] = xr[v] = make_uint4(0, 0, 0, 0);
-                if (c < nvec) {
-                    if (a.dRn) xd[v] = ld_stream_v4(a.dRn + base + c);
-                    xy[v] = ld_stream_v4(a.Y + base + c);
-                    if (a.w2) {
-                        xn[v] = ld_stream_v4(a.dN + base + c);
-                        xr[v] = ld_stream_v4(a.Rn + base + c);
-                    }
-                }
-            }
-            // sums: a n, t e, t n
-            float s[3] = {0.0f, 0.0f, 0.0f};
-            float sgw[kV][kE];  // s g W1
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const int c = v * T + tid;
-                float d[kE], n[kE], y[kE], r[kE], w[kE];
-                E::unpack(xd[v], d);
-                E::unpack(xn[v], n);
-                E::unpack(xy[v], y);
-                E::unpack(xr[v], r);
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    sgw[v][i] = a.scale;
-                    w[i] = 0.0f;
-                }
-                if (c < nvec) {
-                    float f[kE];
-                    if (a.w1) {
-                        E::unpack(__ldg(a.w1 + c), f);
-#pragma unroll
-                        for (int i = 0; i < kE; ++i) sgw[v][i] *= f[i];
-                    }
-                    if (gate) {
-                        E::unpack(__ldg(gate + c), f);
-#pragma unroll
-                        for (int i = 0; i < kE; ++i) sgw[v][i] *= f[i];
-                    }
-                    if (a.w2) E::unpack(__ldg(a.w2 + c), w);
-                }
-#pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    const float nh = r[i] * r2;
-                    const float av = w[i] * n[i];
-                    const float t = sgw[v][i] * (y[i] * r1);
-                    s[0] = fmaf(av, nh, s[0]);
-                    s[1] = fmaf(t, fmaf(r2, av, d[i]), s[1]);
-                    s[2] = fmaf(t, nh, s[2]);
-                    s2[v][i] = fmaf(n[i], nh, s2[v][i]);
-                }
-            }
-            row_sum<3>(s, slots[grp], turn, grp, T);
-            const float k2 = r2 * (s[0] * inv_d);                  // r2 mean(a n)
-            const float c1 = a.w1 ? (s[1] - k2 * s[2]) * inv_d : 0.0f;  // mean(b y)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const int c = v * T + tid;
-                if (c < nvec) {
-                    float d[kE], n[kE], y[kE], r[kE], w[kE], dy[kE];
-                    E::unpack(xd[v], d);
-                    E::unpack(xn[v], n);
-                    E::unpack(xy[v], y);
-                    E::unpack(xr[v], r);
-                    if (a.w2) {
-                        E::unpack(__ldg(a.w2 + c), w);
-#pragma unroll
-                        for (int i = 0; i < kE; ++i)
-                            d[i] = fmaf(r2, w[i] * n[i], d[i]) - k2 * (r[i] * r2);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) {
-                        const float yh = y[i] * r1;
-                        dy[i] = sgw[v][i] * d[i];
-                        if (a.w1) dy[i] = r1 * (dy[i] - yh * c1);
-                        if (kGroups) sg[v][i] = fmaf(d[i], yh, sg[v][i]);
-                        else s1[v][i] = fmaf(d[i], yh, s1[v][i]);
-                    }
-                    st_stream_v4(a.dR + base + c, E::pack(d));
-                    st_stream_v4(a.dY + base + c, E::pack(dy));
-                }
+                fetch_g(v, gate, hold_g[v]);
+                E::unpack2(fetch_w(v), hold_w[v]);
             }
         }
-        if constexpr (kGroups) {
-            // this item's share of the gate row's gradient
+        auto get_g = [&](int v, f2 (&o)[kP]) {
+            if constexpr (kHold) {
+#pragma unroll
+                for (int i = 0; i < kP; ++i) o[i] = hold_g[v][i];
+            } else {
+                fetch_g(v, gate, o);
+            }
+        };
+        auto get_w = [&](int v, f2 (&o)[kP]) {
+            if constexpr (kHold) {
+#pragma unroll
+                for (int i = 0; i < kP; ++i) o[i] = hold_w[v][i];
+            } else {
+                E::unpack2(fetch_w(v), o);
+            }
+        };
+        // a row's statistics are fetched a row ahead
+        float r1n = 1.0f, r2n = 0.0f;
+        auto stats = [&](int64_t row) {
+            if (row >= row1) return;
+            if (a.w1) r1n = __ldg(a.rstd1 + row);
+            if (a.w2) r2n = __ldg(a.rstd2 + row);
+        };
+        stats(row0 + grp);
+        for (int64_t row = row0 + grp; row < row1; row += groups) {
+            const float r1 = r1n, r2 = r2n;
+            stats(row + groups);
+            // (a wait that gave up is recorded; the rows that follow are
+            // worked on all the same, so that the group's barriers match)
+            if (!failed && !mbar_wait(full + 8 * stage, phase, &abort_flag)) {
+                failed = true;
+                if (tid == 0) ring_abandon(full, stages, stage, phase);
+            }
+            const uint32_t st = ring + stage * 4u * pitch + 16u * tid;
+            auto load = [&](int which, int v, f2 (&f)[kP]) { E::unpack2(lds_v4(st + which * pitch + 16u * v * T), f); };
+            // With R, Y unscaled: sums of a R, (s g W1 Y) e and (s g W1 Y) R,
+            // e = dR' + r2 a kept for the second pass
+            f2 e[kHold ? kV : 1][kP];
+            f2 q0 = 0ull, q1 = 0ull, q2 = 0ull;
+            const f2 r22 = pack2(r2, r2);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                f2 n[kP], y[kP], r[kP], w[kP], g[kP];
+                f2 (&ev)[kP] = e[kHold ? v : 0];
+                load(0, v, ev);
+                load(1, v, n);
+                load(2, v, y);
+                load(3, v, r);
+                get_w(v, w);
+                get_g(v, g);
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    const f2 nr = mul2(n[i], r[i]);
+                    q0 = fma2(w[i], nr, q0);
+                    s2[v][i] = fma2(nr, r22, s2[v][i]);
+                    ev[i] = fma2(r22, mul2(w[i], n[i]), ev[i]);
+                    const f2 t = mul2(g[i], y[i]);
+                    q1 = fma2(t, ev[i], q1);
+                    q2 = fma2(t, r[i], q2);
+                }
+            }
+            float s[3] = {lo2(q0) + hi2(q0), lo2(q1) + hi2(q1), lo2(q2) + hi2(q2)};
+            row_sum<3>(s, slots[grp & 7], turn, grp, tid, T);   // (one warp: no slots)
+            __syncwarp();
+            // the whole group is done with the row before this one
+            if (kGates) {
+                if (tid == 0 && !first && stages > 1 && !failed) copy_next();
+                first = false;
+            } else {
+                const int64_t next = row + static_cast<int64_t>(stages - 1) * groups;
+                if (tid == 0 && row >= row0 + groups && stages > 1 && next < row1 && !failed)
+                    copy_row(next, stage > 0 ? stage - 1 : stages - 1);
+            }
+            const float k2 = r2 * (r2 * s[0] * inv_d);                  // r2 mean(a n)
+            const float c1 = r1 * (s[1] - k2 * r2 * s[2]) * inv_d;      // mean(b y)
+            const f2 kr = pack2(-k2 * r2, -k2 * r2), r12 = pack2(r1, r1);
+            const f2 ky = pack2(-c1, -c1);
+            uint4 *dR = a.dR + row * nvec + tid, *dY = a.dY + row * nvec + tid;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                f2 y[kP], r[kP], g[kP], dy[kP];
+                f2 (&ev)[kP] = e[kHold ? v : 0];
+                load(2, v, y);
+                load(3, v, r);
+                get_g(v, g);
+                if constexpr (!kHold) {
+                    f2 n[kP], w[kP];
+                    load(0, v, ev);
+                    load(1, v, n);
+                    get_w(v, w);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) ev[i] = fma2(r22, mul2(w[i], n[i]), ev[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    ev[i] = fma2(kr, r[i], ev[i]);
+                    const f2 yh = mul2(y[i], r12);
+                    sb[v][i] = fma2(ev[i], yh, sb[v][i]);
+                    dy[i] = mul2(ev[i], g[i]);
+                    if (a.w1) dy[i] = mul2(r12, fma2(ky, yh, dy[i]));
+                }
+                if (v * T + tid < nvec) {
+                    st_stream_v4(dR + v * T, E::pack_pairs(ev));
+                    st_stream_v4(dY + v * T, E::pack_pairs(dy));
+                }
+            }
+            if (stages == 1) {
+                if (T > 32) row_barrier(grp, T);
+                else __syncwarp();
+                if (kGates) {
+                    if (tid == 0 && !failed) copy_next();
+                } else if (tid == 0 && row + groups < row1 && !failed) {
+                    copy_row(row + groups, 0);
+                }
+            }
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if constexpr (kGates) {
+            // the item's sum dX y: the row groups' shares meet, in order
+            auto finish = [&](int col, float4 x) {
+                const float4 g = E::load4(a.gate, gr * a.D + col), w = a.w1 ? E::load4(a.w1, col) : ones;
+                const float4 sx = make_float4(a.scale * x.x, a.scale * x.y, a.scale * x.z, a.scale * x.w);
+                if (a.splits == 1)
+                    E::store4(a.dgate, gr * a.D + col, make_float4(w.x * sx.x, w.y * sx.y, w.z * sx.z, w.w * sx.w));
+                else
+                    *reinterpret_cast<float4 *>(a.accg + item * a.D + col) = x;
+                float4 *to = reinterpret_cast<float4 *>(sum1 + col);
+                const float4 o = *to;
+                *to = make_float4(fmaf(g.x, sx.x, o.x), fmaf(g.y, sx.y, o.y), fmaf(g.z, sx.z, o.z),
+                                  fmaf(g.w, sx.w, o.w));
+            };
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 const int c = v * T + tid;
-                if (c < nvec) {
-                    float g[kE], w[kE];
-                    E::unpack(__ldg(gate + c), g);
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) w[i] = 1.0f;
-                    if (a.w1) E::unpack(__ldg(a.w1 + c), w);
-                    if (a.splits == 1) {
-                        float o[kE];
-#pragma unroll
-                        for (int i = 0; i < kE; ++i) o[i] = a.scale * w[i] * sg[v][i];
-                        a.dgate[gr * nvec + c] = E::pack(o);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kE; ++i)
-                            a.accg[item * a.D + static_cast<int64_t>(c) * kE + i] = sg[v][i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) {
-                        s1[v][i] = fmaf(a.scale * g[i], sg[v][i], s1[v][i]);
-                        sg[v][i] = 0.0f;
-                    }
+                for (int i = 0; i < kP; i += 2) {
+                    const float4 x = make_float4(lo2(sb[v][i]), hi2(sb[v][i]), lo2(sb[v][i + 1]), hi2(sb[v][i + 1]));
+                    sb[v][i] = sb[v][i + 1] = 0ull;
+                    if (c >= nvec) continue;
+                    if (groups > 1) *reinterpret_cast<float4 *>(shares + grp * a.D + c * kE + 2 * i) = x;
+                    else finish(c * kE + 2 * i, x);
                 }
+            }
+            if (groups > 1) {
+                block_barrier(T * groups);
+                for (int col = 4 * threadIdx.x; col < a.D; col += 4 * T * groups) {
+                    float4 x = *reinterpret_cast<const float4 *>(shares + col);
+                    for (int k = 1; k < groups; ++k) {
+                        const float4 y = *reinterpret_cast<const float4 *>(shares + k * a.D + col);
+                        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                    }
+                    finish(col, x);
+                }
+                block_barrier(T * groups);
             }
         }
     }
+    griddep_launch_dependents();
+    // The row groups' column sums meet in shared memory (the ring is empty:
+    // every row has been read), group by group in order.
+    float *meet = reinterpret_cast<float *>(smem);
+    if (groups > 1 || kGates) block_barrier(T * groups);
+    if (groups > 1) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const int c = v * T + tid;
+            if (grp > 0 && c < nvec) {
+#pragma unroll
+                for (int i = 0; i < kP; i += 2) {
+                    const int o = (grp - 1) * 2 * a.D + c * kE + 2 * i;
+                    *reinterpret_cast<float4 *>(meet + o) =
+                        make_float4(lo2(s2[v][i]), hi2(s2[v][i]), lo2(s2[v][i + 1]), hi2(s2[v][i + 1]));
+                    if (!kGates)
+                        *reinterpret_cast<float4 *>(meet + o + a.D) =
+                            make_float4(lo2(sb[v][i]), hi2(sb[v][i]), lo2(sb[v][i + 1]), hi2(sb[v][i + 1]));
+                }
+            }
+        }
+        block_barrier(T * groups);
+    }
+    if (failed) atomicOr(&g_block_norm_status, 1u);
+    if (grp > 0) return;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
         const int c = v * T + tid;
         if (c < nvec) {
 #pragma unroll
-            for (int i = 0; i < kE; i += 4) {
-                const int64_t o = me * a.D + static_cast<int64_t>(c) * kE + i;
-                if (a.acc2)
-                    *reinterpret_cast<float4 *>(a.acc2 + o) =
-                        make_float4(s2[v][i], s2[v][i + 1], s2[v][i + 2], s2[v][i + 3]);
-                if (a.acc1)
-                    *reinterpret_cast<float4 *>(a.acc1 + o) =
-                        make_float4(s1[v][i], s1[v][i + 1], s1[v][i + 2], s1[v][i + 3]);
+            for (int i = 0; i < kP; i += 2) {
+                float4 x = make_float4(lo2(s2[v][i]), hi2(s2[v][i]), lo2(s2[v][i + 1]), hi2(s2[v][i + 1]));
+                float4 z = make_float4(lo2(sb[v][i]), hi2(sb[v][i]), lo2(sb[v][i + 1]), hi2(sb[v][i + 1]));
+                for (int g = 0; g + 1 < groups; ++g) {
+                    const float *m = meet + g * 2 * a.D + c * kE + 2 * i;
+                    const float4 p = *reinterpret_cast<const float4 *>(m);
+                    x = make_float4(x.x + p.x, x.y + p.y, x.z + p.z, x.w + p.w);
+                    if (!kGates) {
+                        const float4 q = *reinterpret_cast<const float4 *>(m + a.D);
+                        z = make_float4(z.x + q.x, z.y + q.y, z.z + q.z, z.w + q.w);
+                    }
+                }
+                if (kGates) z = *reinterpret_cast<const float4 *>(sum1 + c * kE + 2 * i);
+                const int64_t o = static_cast<int64_t>(blockIdx.x) * a.D + static_cast<int64_t>(c) * kE + 2 * i;
+                if (a.acc2) *reinterpret_cast<float4 *>(a.acc2 + o) = x;
+                if (a.acc1) *reinterpret_cast<float4 *>(a.acc1 + o) = z;
             }
         }
     }
@@ -378,14 +791,14 @@ struct NormReduceArgs {
     const float *acc2, *acc1, *accg;
     const void *w1, *gate;
     void *dw2, *dw1, *dgate;   // null: not wanted here
-    int64_t workers;
-    int splits;
+    int64_t workers;           // blocks of the main kernel
+    int splits;                // sums per gate row
     int D;
     int per_row;               // per-row gates: acc1 holds dW1 itself, accg the gate rows' sums
     float scale;
 };
 
-constexpr int kReduceRows = 16;
+constexpr int kReduceRows = 32;
 
 // Joins the workers' column sums, in a fixed order: blockIdx.y = 0 the
 // weights (and the single gate row), 1 + g gate row g.
@@ -405,11 +818,13 @@ __global__ void __launch_bounds__(32 * kReduceRows) block_norm_reduce_kernel(con
     const bool gates = blockIdx.y > 0;
     const int64_t gr = static_cast<int64_t>(blockIdx.y) - 1;
     float v0 = 0.0f, v1 = 0.0f;
+    griddep_wait();
     if (col < a.D) {
         if (gates) {
             for (int64_t i = ty; i < a.splits; i += kReduceRows)
                 v0 += a.accg[(gr * a.splits + i) * a.D + col];
         } else {
+#pragma unroll 5
             for (int64_t i = ty; i < a.workers; i += kReduceRows) {
                 if (a.acc2) v0 += a.acc2[i * a.D + col];
                 if (a.acc1) v1 += a.acc1[i * a.D + col];
@@ -454,61 +869,133 @@ RowShape row_shape(int nvec) {
     return s;
 }
 
+// Ring kernels: 16 elements per thread (8 for short rows, 32 for bf16 rows of
+// more than 8192), whole warps per row, row groups up to kRingThreads.
+struct RingShape {
+    int v, T, groups;
+};
+
+RingShape ring_shape(int D, int f32) {
+    RingShape s{};
+    const int nvec = D / (f32 ? 4 : 8), two = f32 ? 4 : 2;   // vectors of 16 elements
+    s.v = nvec <= 64 * two ? two / 2 : (nvec <= 512 * two ? two : 4);
+    s.T = (((nvec + s.v - 1) / s.v) + 31) / 32 * 32;
+    s.groups = kRingThreads / s.T;
+    if (s.groups > kMaxGroups) s.groups = kMaxGroups;   // (T = 32; with more threads it is 8 or fewer)
+    return s;
+}
+
+// Once per kernel and device: opt in to the ring's shared memory.
+template <typename Kernel>
+cudaError_t opt_in(Kernel kernel, std::atomic<unsigned> &mask, const DeviceInfo &dev) {
+    const unsigned bit = 1u << (dev.device & 31);
+    if (mask.load() & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingRoom));
+    if (e == cudaSuccess) mask.fetch_or(bit);
+    return e;
+}
+
 struct BwdPlan {
-    RowShape rows;
-    int64_t workers, splits, blocks;
+    int v, T, groups, stages;
+    uint32_t smem;
+    int64_t splits, blocks;
     size_t bytes;
 };
 
-// Workers: up to two blocks per SM, at least eight rows each (each worker
-// costs 8 D bytes of column sums written and read again).
-BwdPlan bwd_plan(int64_t M, int D, int dtype_f32, bool per_row, int64_t groups, bool w1, bool w2,
-                 bool gate, int sm_count) {
+// One block per SM: as many row groups as its threads hold (their column sums
+// meet in the block, so a block costs 8 D bytes of sums written and read
+// again, however many rows it takes at a time), rings over all of its shared
+// memory.  At least `groups` rows per block.
+BwdPlan bwd_plan(int64_t M, int D, int f32, bool per_row, int64_t gates, bool w1, bool w2, bool gate,
+                 int sm_count) {
     BwdPlan p{};
-    p.rows = row_shape(D / (dtype_f32 ? 4 : 8));
-    int64_t want = static_cast<int64_t>(sm_count) * 2 * p.rows.groups;
-    const int64_t most = (M + 7) / 8;
-    if (want > most) want = most;
-    if (want < 1) want = 1;
-    p.splits = per_row ? (want / groups > 0 ? want / groups : 1) : want;
-    const int64_t rows_per_group = per_row ? M / groups : M;
-    if (p.splits > rows_per_group) p.splits = rows_per_group;
+    const RingShape sh = ring_shape(D, f32);
+    p.v = sh.v;
+    p.T = sh.T;
+    p.groups = sh.groups;
+    constexpr uint32_t kRoom = kRingRoom;
+    const uint32_t row = 4u * 16u * p.v * p.T;   // (operands are padded to whole warps)
+    const int64_t rows_per_gate = per_row ? M / gates : M;
+    auto sums = [&]() { return per_row ? 4u * D * (1u + (p.groups > 1 ? p.groups : 0u)) : 0u; };
+    while (p.groups > 1 && (p.groups * row * 2u + sums() > kRoom || p.groups > rows_per_gate)) --p.groups;
+    p.stages = static_cast<int>((kRoom - sums()) / (row * p.groups));
+    if (p.stages > kMaxRing) p.stages = kMaxRing;
+    p.smem = p.stages * row * p.groups + sums();
+    const int64_t most = (rows_per_gate + p.groups - 1) / p.groups;
+    p.splits = per_row ? sm_count / gates : sm_count;
+    if (p.splits > most) p.splits = most;
     if (p.splits < 1) p.splits = 1;
-    const int64_t items = (per_row ? groups : 1) * p.splits;
-    if (want > items) want = items;
-    p.blocks = (want + p.rows.groups - 1) / p.rows.groups;
-    p.workers = p.blocks * p.rows.groups;
+    const int64_t items = (per_row ? gates : 1) * p.splits;
+    p.blocks = items < sm_count ? items : sm_count;
     size_t floats = 0;
-    if (w2) floats += static_cast<size_t>(p.workers) * D;
-    if (w1 || (gate && !per_row)) floats += static_cast<size_t>(p.workers) * D;
+    if (w2) floats += static_cast<size_t>(p.blocks) * D;
+    if (w1 || (gate && !per_row)) floats += static_cast<size_t>(p.blocks) * D;
     if (per_row && p.splits > 1) floats += static_cast<size_t>(items) * D;
     p.bytes = floats * 4;
     return p;
 }
 
-template <bool kBf16>
-void launch_fwd(const NormArgs &a, int sm_count, cudaStream_t stream) {
-    const RowShape s = row_shape(a.D / Vec<kBf16>::kE);
-    const dim3 block(s.T, s.groups);
+template <bool kBf16, int kV>
+cudaError_t launch_fwd_ring(const NormArgs &a, const RingShape &s, const DeviceInfo &dev, cudaStream_t stream) {
+    static std::atomic<unsigned> mask{0};
+    auto kernel = block_norm_ring_kernel<kBf16, kV>;
+    const cudaError_t e = opt_in(kernel, mask, dev);
+    if (e != cudaSuccess) return e;
+    const uint32_t row = 2u * 16u * s.v * s.T;
+    int stages = static_cast<int>(kRingRoom / (row * s.groups));
+    if (stages > kMaxRing) stages = kMaxRing;
+    kernel<<<dev.sm_count, s.T * s.groups, stages * row * s.groups, stream>>>(a, s.T, s.groups, stages);
+    return cudaGetLastError();
+}
+
+template <bool kBf16, int kV>
+cudaError_t launch_fwd_v(const NormArgs &a, const RowShape &s, int sm_count, cudaStream_t stream) {
     int64_t blocks = (a.M + s.groups - 1) / s.groups;
     const int64_t most = static_cast<int64_t>(sm_count) * (2048 / (s.T * s.groups));
     if (blocks > most) blocks = most;
-    const unsigned g = static_cast<unsigned>(blocks);
+    block_norm_kernel<kBf16, kV><<<static_cast<unsigned>(blocks), dim3(s.T, s.groups), 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool kBf16>
+cudaError_t launch_fwd(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
+    const RingShape r = ring_shape(a.D, !kBf16);
+    const int nvec = a.D / Vec<kBf16>::kE;
+    // Rings for rows of 8 KB up to what holds its weights in registers, from
+    // four rows per row group on.  Ring against plain, B200: M = 8192,
+    // D = 4096 bf16 50.0 against 52.8 us; M = 777, D = 5120 fp32 12.7 against
+    // 17.0; outside, M = 512, D = 4096 6.3 against 4.9; M = 4096, D = 1024
+    // 11.9 against 9.9; M = 2048, D = 16384 75 against 67.
+    if (nvec >= 512 && r.v * Vec<kBf16>::kE <= 16 && a.M >= 4 * static_cast<int64_t>(dev.sm_count) * r.groups)
+        return launch_fwd_ring<kBf16, kBf16 ? 2 : 4>(a, r, dev, stream);
+    const RowShape s = row_shape(nvec);
     switch (s.v) {
-        case 1: block_norm_kernel<kBf16, 1><<<g, block, 0, stream>>>(a); break;
-        case 2: block_norm_kernel<kBf16, 2><<<g, block, 0, stream>>>(a); break;
-        default: block_norm_kernel<kBf16, 4><<<g, block, 0, stream>>>(a); break;
+        case 1: return launch_fwd_v<kBf16, 1>(a, s, dev.sm_count, stream);
+        case 2: return launch_fwd_v<kBf16, 2>(a, s, dev.sm_count, stream);
+        default: return launch_fwd_v<kBf16, 4>(a, s, dev.sm_count, stream);
     }
 }
 
-template <bool kBf16, bool kGroups>
-void launch_bwd(const NormBwdArgs &a, const BwdPlan &p, cudaStream_t stream) {
-    const dim3 block(p.rows.T, p.rows.groups);
-    const unsigned g = static_cast<unsigned>(p.blocks);
-    switch (p.rows.v) {
-        case 1: block_norm_bwd_kernel<kBf16, 1, kGroups><<<g, block, 0, stream>>>(a); break;
-        case 2: block_norm_bwd_kernel<kBf16, 2, kGroups><<<g, block, 0, stream>>>(a); break;
-        default: block_norm_bwd_kernel<kBf16, 4, kGroups><<<g, block, 0, stream>>>(a); break;
+template <bool kBf16, int kV, bool kGates>
+cudaError_t launch_bwd_v(const NormBwdArgs &a, const BwdPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
+    static std::atomic<unsigned> mask{0};
+    auto kernel = block_norm_bwd_kernel<kBf16, kV, kGates>;
+    const cudaError_t e = opt_in(kernel, mask, dev);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(p.blocks), p.T * p.groups, p.smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool kGates>
+cudaError_t launch_bwd(int f32, const NormBwdArgs &a, const BwdPlan &p, const DeviceInfo &dev, cudaStream_t stream) {
+    if (f32)
+        return p.v == 2 ? launch_bwd_v<false, 2, kGates>(a, p, dev, stream)
+                        : launch_bwd_v<false, 4, kGates>(a, p, dev, stream);
+    switch (p.v) {
+        case 1: return launch_bwd_v<true, 1, kGates>(a, p, dev, stream);
+        case 2: return launch_bwd_v<true, 2, kGates>(a, p, dev, stream);
+        default: return launch_bwd_v<true, 4, kGates>(a, p, dev, stream);
     }
 }
 
@@ -532,9 +1019,7 @@ cudaError_t launch_block_norm(const void *Y, const void *R, const BlockNorm &n, 
     a.D = D;
     a.scale = n.scale;
     a.eps = n.eps;
-    if (f32) launch_fwd<false>(a, dev.sm_count, stream);
-    else launch_fwd<true>(a, dev.sm_count, stream);
-    return cudaGetLastError();
+    return f32 ? launch_fwd<false>(a, dev, stream) : launch_fwd<true>(a, dev, stream);
 }
 
 size_t block_norm_bwd_workspace(int64_t M, int D, int f32, const BlockNorm &n, int sm_count) {
@@ -548,8 +1033,8 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
                                   void *workspace, int64_t M, int D, int f32,
                                   const DeviceInfo &dev, cudaStream_t stream) {
     const bool per_row = n.gate && n.gate_rows > 1;
-    const int64_t groups = per_row ? n.gate_rows : 1;
-    const BwdPlan p = bwd_plan(M, D, f32, per_row, groups, n.w1, n.w2, n.gate, dev.sm_count);
+    const int64_t gates = per_row ? n.gate_rows : 1;
+    const BwdPlan p = bwd_plan(M, D, f32, per_row, gates, n.w1, n.w2, n.gate, dev.sm_count);
     float *ws = static_cast<float *>(workspace);
     NormBwdArgs a{};
     a.dRn = static_cast<const uint4 *>(dRn);
@@ -564,7 +1049,7 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
     a.dY = static_cast<uint4 *>(dY);
     a.dR = static_cast<uint4 *>(dR);
     a.dgate = static_cast<uint4 *>(dgate);
-    const size_t per = static_cast<size_t>(p.workers) * D;
+    const size_t per = static_cast<size_t>(p.blocks) * D;
     if (n.w2) {
         a.acc2 = ws;
         ws += per;
@@ -574,19 +1059,15 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
         ws += per;
     }
     if (per_row && p.splits > 1) a.accg = ws;
-    a.rows_per_gate = per_row ? M / groups : M;
-    a.groups = groups;
+    a.rows_per_gate = per_row ? M / gates : M;
+    a.gates = gates;
     a.splits = static_cast<int>(p.splits);
     a.D = D;
+    a.T = p.T;
+    a.groups = p.groups;
     a.scale = n.scale;
-    if (f32) {
-        if (per_row) launch_bwd<false, true>(a, p, stream);
-        else launch_bwd<false, false>(a, p, stream);
-    } else {
-        if (per_row) launch_bwd<true, true>(a, p, stream);
-        else launch_bwd<true, false>(a, p, stream);
-    }
-    cudaError_t e = cudaGetLastError();
+    a.stages = p.stages;
+    cudaError_t e = per_row ? launch_bwd<true>(f32, a, p, dev, stream) : launch_bwd<false>(f32, a, p, dev, stream);
     if (e != cudaSuccess || !(a.acc2 || a.acc1 || a.accg)) return e;
     NormReduceArgs r{};
     r.acc2 = a.acc2;
@@ -597,16 +1078,35 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
     r.dw2 = n.w2 ? dw2 : nullptr;
     r.dw1 = n.w1 ? dw1 : nullptr;
     r.dgate = n.gate ? dgate : nullptr;
-    r.workers = p.workers;
-    r.splits = a.splits;
+    r.workers = p.blocks;
+    r.splits = static_cast<int>(p.splits);
     r.D = D;
     r.per_row = per_row ? 1 : 0;
     r.scale = n.scale;
-    const dim3 grid((D + 31) / 32, static_cast<unsigned>(1 + (a.accg ? groups : 0)));
+    const dim3 grid((D + 31) / 32, static_cast<unsigned>(1 + (a.accg ? gates : 0)));
     const dim3 block(32, kReduceRows);
-    if (f32) block_norm_reduce_kernel<false><<<grid, block, 0, stream>>>(r);
-    else block_norm_reduce_kernel<true><<<grid, block, 0, stream>>>(r);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return f32 ? cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel<false>, r)
+               : cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel<true>, r);
+}
+
+cudaError_t block_norm_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_block_norm_status, sizeof(unsigned int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_block_norm_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice,
+                                stream);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(stream);
 }
 
 }  // namespace swiglu

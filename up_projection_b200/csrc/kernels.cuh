@@ -171,6 +171,8 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
                                   void *workspace, int64_t M, int D, int f32,
                                   const DeviceInfo &dev, cudaStream_t stream);
 
+cudaError_t block_norm_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream);
+
 // e4m3 quantisation in blocks of 128 (quant_b128.cu) and the products of
 // such operands (gemm_b128.cu).
 cudaError_t launch_quant_b128(const void *X, void *Q, float *S, int64_t R, int C, int f32,
