@@ -377,7 +377,7 @@ def _fits(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
 def _codes(t: torch.Tensor, name: str):
     if not (t.is_cuda and t.is_contiguous()):
         _dev(t, name)
-    if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn)")
 
 
@@ -412,15 +412,19 @@ def swiglu_quant_b128(X: torch.Tensor, block: str = "row", transpose: bool = Fal
     C = shape[-1]
     R = X.numel() // C if C else math.prod(shape[:-1])
     rows, cols = (C, (R + 15) // 16 * 16) if transpose else (R, C)
-    Q = torch.empty((rows, cols) if transpose else shape, dtype=torch.uint8, device=X.device)
+    Q = X.new_empty((rows, cols) if transpose else shape, dtype=torch.uint8)
     kb = (cols + 127) // 128
-    S = torch.empty(((rows + 127) // 128, kb) if tile else (kb, (rows + 3) // 4 * 4), dtype=torch.float32,
-                    device=X.device)
+    if tile:
+        S = X.new_empty(((rows + 127) // 128, kb), dtype=torch.float32)
+    elif rows & 3 or not kb:
+        S = X.new_empty((kb, (rows + 3) // 4 * 4), dtype=torch.float32)[:, :rows].t()
+    else:
+        S = X.new_empty_strided((rows, kb), (1, rows), dtype=torch.float32)
     st = lib().swiglu_quant_b128(X.data_ptr(), Q.data_ptr(), S.data_ptr(), R, C, code,
                                  1 if tile else 0, 1 if transpose else 0, _stream(stream))
     if st:
         _check("swiglu_quant_b128", st)
-    return Q, S if tile else S[:, :rows].t()
+    return Q, S
 
 
 def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: torch.Tensor,
@@ -443,8 +447,9 @@ def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: tor
     rows = (N + 127) // 128
     if Bs.shape == (rows, kb):
         block = SWIGLU_BLOCK_TILE
-        _dev(Bs, "Bs")
-        if Bs.dtype != torch.float32:
+        if not (Bs.is_cuda and Bs.is_contiguous()):
+            _dev(Bs, "Bs")
+        if Bs.dtype is not torch.float32:
             raise TypeError("Bs must be float32")
     else:
         block = SWIGLU_BLOCK_ROW
@@ -454,7 +459,7 @@ def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: tor
         raise TypeError(f"unsupported out_dtype {out_dtype}; use bfloat16 or float32")
     _here(A, As, B, Bs, Y)
     if Y is None:
-        Y = torch.empty((*A.shape[:-1], N), dtype=out_dtype, device=A.device)
+        Y = A.new_empty((*A.shape[:-1], N), dtype=out_dtype)
     else:
         _dev(Y, "Y")
         if Y.dtype != out_dtype or Y.numel() != M * N:
@@ -473,22 +478,26 @@ def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: to
     """swiglu_fwd on block-scaled e4m3 operands: X [..., K] codes with 1 x 128
     scales Xs [M, KB], Wg, Wu [N, K] codes with 128 x 128 scales
     [ceil(N/128), KB].  Returns H bf16 [..., N], or (H, G, U)."""
-    for t, n in ((X, "X"), (Wg, "Wg"), (Wu, "Wu")):
-        _codes(t, n)
+    _codes(X, "X")
+    _codes(Wg, "Wg")
+    _codes(Wu, "Wu")
     K = X.shape[-1]
     M = math.prod(X.shape[:-1])
-    N = Wg.shape[0]
-    if Wg.shape != (N, K) or Wu.shape != (N, K):
+    w = Wg.shape
+    N = w[0]
+    if w != (N, K) or Wu.shape != w:
         raise ValueError(f"weights must be [N, K] = [{N}, {K}]")
     kb = (K + 127) // 128
     _row_scales(Xs, "Xs", M, kb)
-    for t, n in ((Wgs, "Wgs"), (Wus, "Wus")):
-        _dev(t, n)
-        if t.dtype != torch.float32 or t.shape != ((N + 127) // 128, kb):
-            raise ValueError(f"{n} must be float32 [{(N + 127) // 128}, {kb}]")
+    tiles = ((N + 127) // 128, kb)
+    if not (_fits(Wgs, torch.float32, tiles) and _fits(Wus, torch.float32, tiles)):
+        for t, n in ((Wgs, "Wgs"), (Wus, "Wus")):
+            _dev(t, n)
+            if t.dtype != torch.float32 or t.shape != tiles:
+                raise ValueError(f"{n} must be float32 [{tiles[0]}, {kb}]")
     _here(X, Xs, Wg, Wgs, Wu, Wus, H)
     if H is None:
-        H = torch.empty((*X.shape[:-1], N), dtype=torch.bfloat16, device=X.device)
+        H = X.new_empty((*X.shape[:-1], N), dtype=torch.bfloat16)
     else:
         _dev(H, "H")
         if H.dtype != torch.bfloat16 or H.numel() != M * N:
@@ -568,9 +577,9 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
     r1 = r2 = None
     if return_stats:
         if post_weight is not None:
-            r1 = torch.empty((M,), dtype=torch.float32, device=Y.device)
+            r1 = Y.new_empty((M,), dtype=torch.float32)
         if pre_weight is not None:
-            r2 = torch.empty((M,), dtype=torch.float32, device=Y.device)
+            r2 = Y.new_empty((M,), dtype=torch.float32)
     st = lib().swiglu_block_norm(Y.data_ptr(), R.data_ptr(), ctypes.byref(p), Rn.data_ptr(),
                                  N.data_ptr() if N is not None else None,
                                  r1.data_ptr() if r1 is not None else None,
@@ -624,7 +633,7 @@ def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: 
     ws = None
     if need > 0:
         # drawn on the current stream; a different stream of the call keeps it
-        ws = torch.empty((need,), dtype=torch.uint8, device=Y.device)
+        ws = Y.new_empty((need,), dtype=torch.uint8)
     s = _stream(stream)
     if ws is not None and stream is not None and s != torch.cuda.current_stream().cuda_stream:
         ext = torch.cuda.ExternalStream(s, device=Y.device)
