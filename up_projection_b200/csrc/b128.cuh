@@ -134,48 +134,15 @@ __device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// A warp's 32 rows x 64 bytes to global memory through its staging buffer:
-// lane = row writes its four 16-byte chunks (swizzled over the banks), then
-// every four lanes store 64 consecutive bytes of a row.  `cols16` of the four
-// chunks belong to the tile.
-__device__ __forceinline__ void store_rows(uint32_t buf, int lane, const uint4 (&v)[4], char *dst,
-                                           int64_t row_bytes, int rows, int cols16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        sts_v4(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), v[j]);
-    __syncwarp();
-    const int j = lane & 3;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int r = it * 8 + (lane >> 2);
-        const uint4 w = lds_v4(buf + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
-        if (r < rows && j < cols16) *reinterpret_cast<uint4 *>(dst + r * row_bytes + j * 16) = w;
-    }
-    __syncwarp();
-}
-
-// One block's 32 accumulator columns of a warp, times their scales, into the
-// running sums.  Tile scales: the four units of 8 columns take slo below
-// unit `cut` (counted from these columns) and shi from there on.
-__device__ __forceinline__ void add_tile(unsigned long long (&acc)[16], const uint32_t (&v)[32],
-                                         float slo, float shi, int cut) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float s = u < cut ? slo : shi;
-        const unsigned long long s2 = pair2(s, s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fma2(acc[4 * u + i], v[8 * u + 2 * i], v[8 * u + 2 * i + 1], s2);
-    }
-}
-
-// The same with one scale for all 32 columns.
+// One block's 32 accumulator columns of a warp, times their one scale, into the
+// running sums.
 __device__ __forceinline__ void add_block(unsigned long long (&acc)[16], const uint32_t (&v)[32], float s) {
     const unsigned long long s2 = pair2(s, s);
 #pragma unroll
     for (int i = 0; i < 16; ++i) fma2(acc[i], v[2 * i], v[2 * i + 1], s2);
 }
 
-// Row scales: one per column, in shared memory at sb.
+// The same with row scales: one per column, in shared memory at sb.
 __device__ __forceinline__ void add_rows(unsigned long long (&acc)[16], const uint32_t (&v)[32],
                                          float sa, uint32_t sb) {
     const unsigned long long sa2 = pair2(sa, sa);
@@ -186,65 +153,6 @@ __device__ __forceinline__ void add_rows(unsigned long long (&acc)[16], const ui
         const unsigned long long s1 = pair2(__uint_as_float(w.z), __uint_as_float(w.w));
         fma2(acc[2 * i], v[4 * i], v[4 * i + 1], mul2(s0, sa2));
         fma2(acc[2 * i + 1], v[4 * i + 2], v[4 * i + 3], mul2(s1, sa2));
-    }
-}
-
-// A warp's share of a tile, from its sums to global memory: rows row0 .. (at
-// most 32, `rows` of them), columns colg .. of `mine` units of 8.  acc[0..3]:
-// groups of 32 columns (gated: 0, 1 of G and 2, 3 of U).
-template <int kMode>
-__device__ __forceinline__ void store_tile(const unsigned long long (&acc)[4][16], const Out &out,
-                                           uint32_t buf, int lane, int64_t row0, int64_t colg, int N,
-                                           int rows, int mine) {
-    auto put_bf16 = [&](void *y, int group, int units_left, auto value) {
-        uint4 v[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            v[c] = make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3));
-        store_rows(buf, lane, v, static_cast<char *>(y) + 2 * (row0 * N + colg + 32 * group), 2ll * N,
-                   rows, units_left);
-    };
-    if constexpr (kMode == kGated) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int left = mine - 4 * j;
-            if (left > 0) {
-                put_bf16(out.y, j, left, [&](int i) {
-                    return pack_bf16x2(
-                        act::gated<false>(out.act, out.alpha, lo2(acc[j][i]), lo2(acc[2 + j][i])),
-                        act::gated<false>(out.act, out.alpha, hi2(acc[j][i]), hi2(acc[2 + j][i])));
-                });
-                if (out.g) {
-                    put_bf16(out.g, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
-                    put_bf16(out.u, j, left,
-                             [&](int i) { return pack_bf16x2(lo2(acc[2 + j][i]), hi2(acc[2 + j][i])); });
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int left = mine - 4 * j;
-            if (left > 0) {
-                if (!out.f32) {
-                    put_bf16(out.y, j, left, [&](int i) { return pack_bf16x2(lo2(acc[j][i]), hi2(acc[j][i])); });
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // 16 columns = 64 bytes each
-                        uint4 v[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const unsigned long long a0 = acc[j][8 * h + 2 * c], a1 = acc[j][8 * h + 2 * c + 1];
-                            v[c] = make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
-                                              static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32));
-                        }
-                        store_rows(buf, lane, v,
-                                   static_cast<char *>(out.y) + 4 * (row0 * N + colg + 32 * j + 16 * h),
-                                   4ll * N, rows, 2 * (left - 2 * h));
-                    }
-                }
-            }
-        }
     }
 }
 

@@ -10,7 +10,8 @@
 // MMAs (K = 32) per block whatever M is, and lane n of the accumulator holds
 // output column n for all rows of A.  (B200, M = 8, N = 4096, K = 14336, 58.7 MB
 // of weights: A as the M operand 29.8 us; warp-level mma.sync, which unpacks
-// e4m3 to fp16 first, 22.3 us; this form PLACEHOLDER us.)
+// e4m3 to fp16 first, 22.3 us; this form 17.7 us, of 13 us that the copies alone
+// take.)
 //
 // A tile is R rows of weights (a multiple of 8, at most 256: two MMAs per
 // step), spread evenly over the SMs; where that would leave few rows per SM,
