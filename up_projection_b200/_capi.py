@@ -369,21 +369,34 @@ def _here(*tensors):
             raise ValueError(f"all tensors must be on the current device (cuda:{i})")
 
 
-def _fits(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
-    """One cheap pass over what every operand needs (messages only on failure)."""
-    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
-def _codes(t: torch.Tensor, name: str):
-    if not (t.is_cuda and t.is_contiguous()):
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The current device, which the contiguous tensor t is on."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_contiguous():
         _dev(t, name)
+    if dev != _raw_device():
+        _here(t)
+    return dev
+
+
+def _fits(t: torch.Tensor, device: int, dtype: torch.dtype, shape) -> bool:
+    """One cheap pass over what every operand needs (messages only on failure)."""
+    return t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _codes(t: torch.Tensor, name: str, device: int):
+    if t.get_device() != device or not t.is_contiguous():
+        _dev(t, name)
+        _here(t)
     if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn)")
 
 
-def _row_scales(s: torch.Tensor, name: str, rows: int, kb: int):
+def _row_scales(s: torch.Tensor, name: str, rows: int, kb: int, device: int):
     """The 1 x 128 scales [rows, kb], stored [kb, rows padded to 4]."""
-    if not s.is_cuda or s.dtype != torch.float32 or s.shape != (rows, kb):
+    if s.get_device() != device or s.dtype is not torch.float32 or s.shape != (rows, kb):
+        if s.is_cuda:
+            _here(s)
         raise ValueError(f"{name} must be a float32 CUDA tensor [{rows}, {kb}]")
     if rows and kb and ((rows > 1 and s.stride(0) != 1) or
                         (kb > 1 and s.stride(1) != (rows + 3) // 4 * 4)):
@@ -435,33 +448,33 @@ def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: tor
     Bs [ceil(N/128), KB] (128 x 128 blocks) or [N, KB] (1 x 128, rows innermost
     in memory); KB = ceil(K/128), K a multiple of 16, N of 8.  Y bf16 or fp32
     with A's leading dims."""
-    _codes(A, "A")
-    _codes(B, "B")
-    K = A.shape[-1]
-    M = math.prod(A.shape[:-1])
+    dev = _device_of(A, "A")
+    _codes(A, "A", dev)
+    _codes(B, "B", dev)
+    shape = A.shape
+    K = shape[-1]
+    M = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     N = B.shape[0]
     if B.shape != (N, K):
         raise ValueError(f"B must be [N, K] = [{N}, {K}]")
     kb = (K + 127) // 128
-    _row_scales(As, "As", M, kb)
-    rows = (N + 127) // 128
-    if Bs.shape == (rows, kb):
+    _row_scales(As, "As", M, kb, dev)
+    tiles = ((N + 127) // 128, kb)
+    if Bs.shape == tiles:
         block = SWIGLU_BLOCK_TILE
-        if not (Bs.is_cuda and Bs.is_contiguous()):
-            _dev(Bs, "Bs")
-        if Bs.dtype is not torch.float32:
-            raise TypeError("Bs must be float32")
+        if not _fits(Bs, dev, torch.float32, tiles):
+            _refuse(Bs, "Bs", f"float32 [{tiles[0]}, {kb}]")
     else:
         block = SWIGLU_BLOCK_ROW
-        _row_scales(Bs, "Bs", N, kb)
+        _row_scales(Bs, "Bs", N, kb, dev)
     code = _DT.get(out_dtype)
     if code is None:
         raise TypeError(f"unsupported out_dtype {out_dtype}; use bfloat16 or float32")
-    _here(A, As, B, Bs, Y)
     if Y is None:
-        Y = A.new_empty((*A.shape[:-1], N), dtype=out_dtype)
+        Y = A.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
     else:
         _dev(Y, "Y")
+        _here(Y)
         if Y.dtype != out_dtype or Y.numel() != M * N:
             raise ValueError("Y has the wrong dtype or size")
     st = lib().swiglu_gemm_b128(A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(),
@@ -478,71 +491,86 @@ def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: to
     """swiglu_fwd on block-scaled e4m3 operands: X [..., K] codes with 1 x 128
     scales Xs [M, KB], Wg, Wu [N, K] codes with 128 x 128 scales
     [ceil(N/128), KB].  Returns H bf16 [..., N], or (H, G, U)."""
-    _codes(X, "X")
-    _codes(Wg, "Wg")
-    _codes(Wu, "Wu")
-    K = X.shape[-1]
-    M = math.prod(X.shape[:-1])
+    dev = _device_of(X, "X")
+    _codes(X, "X", dev)
+    _codes(Wg, "Wg", dev)
+    _codes(Wu, "Wu", dev)
+    shape = X.shape
+    K = shape[-1]
+    M = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     w = Wg.shape
     N = w[0]
     if w != (N, K) or Wu.shape != w:
         raise ValueError(f"weights must be [N, K] = [{N}, {K}]")
     kb = (K + 127) // 128
-    _row_scales(Xs, "Xs", M, kb)
+    _row_scales(Xs, "Xs", M, kb, dev)
     tiles = ((N + 127) // 128, kb)
-    if not (_fits(Wgs, torch.float32, tiles) and _fits(Wus, torch.float32, tiles)):
-        for t, n in ((Wgs, "Wgs"), (Wus, "Wus")):
-            _dev(t, n)
-            if t.dtype != torch.float32 or t.shape != tiles:
-                raise ValueError(f"{n} must be float32 [{tiles[0]}, {kb}]")
-    _here(X, Xs, Wg, Wgs, Wu, Wus, H)
+    if not _fits(Wgs, dev, torch.float32, tiles):
+        _refuse(Wgs, "Wgs", f"float32 [{tiles[0]}, {kb}]")
+    if not _fits(Wus, dev, torch.float32, tiles):
+        _refuse(Wus, "Wus", f"float32 [{tiles[0]}, {kb}]")
     if H is None:
-        H = X.new_empty((*X.shape[:-1], N), dtype=torch.bfloat16)
+        H = X.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=torch.bfloat16)
     else:
         _dev(H, "H")
+        _here(H)
         if H.dtype != torch.bfloat16 or H.numel() != M * N:
             raise ValueError("H has the wrong dtype or size")
-    G = U = None
+    G = U = epi = None   # (no epilogue: silu, multiplier 1, neither G nor U)
     if return_gu:
         G = torch.empty_like(H)
         U = torch.empty_like(H)
-    epi = Epilogue(int(activation), float(gate_multiplier), G.data_ptr() if return_gu else None,
-                   U.data_ptr() if return_gu else None)
+    if return_gu or activation != SWIGLU_ACT_SILU or gate_multiplier != 1.0:
+        epi = ctypes.byref(Epilogue(int(activation), float(gate_multiplier),
+                                    G.data_ptr() if return_gu else None, U.data_ptr() if return_gu else None))
     st = lib().swiglu_fwd_b128(X.data_ptr(), Xs.data_ptr(), Wg.data_ptr(), Wgs.data_ptr(),
-                               Wu.data_ptr(), Wus.data_ptr(), H.data_ptr(), M, K, N,
-                               ctypes.byref(epi), _stream(stream))
+                               Wu.data_ptr(), Wus.data_ptr(), H.data_ptr(), M, K, N, epi, _stream(stream))
     if st:
         _check("swiglu_fwd_b128", st)
     return (H, G, U) if return_gu else H
 
 
-def _norm_params(dt, D, post_weight, pre_weight, gate, residual_scale, eps):
+def _refuse(t: torch.Tensor, name: str, what: str):
+    """What _fits found wrong with an operand."""
+    _dev(t, name)
+    _here(t)
+    raise ValueError(f"{name} must be {what}")
+
+
+def _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, eps):
     """The checked parameter struct of the block norm calls."""
     w1 = w2 = g = None
     rows = 1
     if post_weight is not None:
-        if not _fits(post_weight, dt, (D,)):
-            _dev(post_weight, "post_weight")
-            raise ValueError(f"post_weight must be [{D}] of Y's dtype")
+        if not _fits(post_weight, dev, dt, (D,)):
+            _refuse(post_weight, "post_weight", f"[{D}] of Y's dtype")
         w1 = post_weight.data_ptr()
     if pre_weight is not None:
-        if not _fits(pre_weight, dt, (D,)):
-            _dev(pre_weight, "pre_weight")
-            raise ValueError(f"pre_weight must be [{D}] of Y's dtype")
+        if not _fits(pre_weight, dev, dt, (D,)):
+            _refuse(pre_weight, "pre_weight", f"[{D}] of Y's dtype")
         w2 = pre_weight.data_ptr()
     if gate is not None:
-        if gate.dim() > 2 or not _fits(gate, dt, (*gate.shape[:-1], D)):
-            _dev(gate, "gate")
-            raise ValueError(f"gate must be [{D}] or [rows, {D}] of Y's dtype")
-        rows = gate.numel() // D if D else 1
+        if gate.dim() == 2:
+            rows = gate.shape[0]
+            ok = _fits(gate, dev, dt, (rows, D))
+        else:
+            ok = _fits(gate, dev, dt, (D,))
+        if not ok:
+            _refuse(gate, "gate", f"[{D}] or [rows, {D}] of Y's dtype")
         g = gate.data_ptr()
     return BlockNormParams(w1, w2, g, rows, residual_scale, eps)
 
 
-def _same(t, like, name):
-    if not _fits(t, like.dtype, like.shape):
-        _dev(t, name)
-        raise ValueError(f"{name} must have Y's dtype and shape")
+def _norm_shape(Y):
+    """Device, dtype, its code, M and D of a block norm's Y."""
+    dev = _device_of(Y, "Y")
+    dt = Y.dtype
+    code = _DT.get(dt)
+    if code is None:
+        _dtype_code(Y)
+    shape = Y.shape
+    D = shape[-1]
+    return dev, dt, code, shape, Y.numel() // D if D else 0, D
 
 
 def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tensor | None = None,
@@ -558,21 +586,14 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
     m // (M / rows)).  Returns (Rn, N), with return_stats=True (training)
     (Rn, N, rstd_post, rstd_pre), fp32 [M], for swiglu_block_norm_bwd.  Rn may
     be given as the output buffer, R itself included (in place)."""
-    if not (Y.is_cuda and Y.is_contiguous()):
-        _dev(Y, "Y")
-    _same(R, Y, "R")
-    dt = Y.dtype
-    code = _DT.get(dt)
-    if code is None:
-        _dtype_code(Y)
-    D = Y.shape[-1]
-    M = Y.numel() // D if D else 0
-    p = _norm_params(dt, D, post_weight, pre_weight, gate, residual_scale, eps)
-    _here(Y, R, post_weight, pre_weight, gate, Rn)
+    dev, dt, code, shape, M, D = _norm_shape(Y)
+    if not _fits(R, dev, dt, shape):
+        _refuse(R, "R", "of Y's dtype and shape")
+    p = _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, eps)
     if Rn is None:
         Rn = torch.empty_like(R)
-    else:
-        _same(Rn, Y, "Rn")
+    elif not _fits(Rn, dev, dt, shape):
+        _refuse(Rn, "Rn", "of Y's dtype and shape")
     N = torch.empty_like(Y) if pre_weight is not None else None
     r1 = r2 = None
     if return_stats:
@@ -599,30 +620,19 @@ def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: 
     d_pre, d_gate), the last three None without their parameter (d_gate has
     gate's shape).  dRn or dN may be None for zero (dN only without
     pre_weight); Rn, rstd_post, rstd_pre as the forward returned them."""
-    if not (Y.is_cuda and Y.is_contiguous()):
-        _dev(Y, "Y")
-    _same(Rn, Y, "Rn")
-    dt = Y.dtype
-    code = _DT.get(dt)
-    if code is None:
-        _dtype_code(Y)
-    D = Y.shape[-1]
-    M = Y.numel() // D if D else 0
-    if dRn is not None:
-        _same(dRn, Y, "dRn")
+    dev, dt, code, shape, M, D = _norm_shape(Y)
     if (dN is None) != (pre_weight is None):
         raise ValueError("dN and pre_weight go together")
-    if dN is not None:
-        _same(dN, Y, "dN")
+    for t, n in ((Rn, "Rn"), (dRn, "dRn"), (dN, "dN")):
+        if t is not None and not _fits(t, dev, dt, shape):
+            _refuse(t, n, "of Y's dtype and shape")
     for w, t, n in ((post_weight, rstd_post, "rstd_post"), (pre_weight, rstd_pre, "rstd_pre")):
         if w is not None:
             if t is None:
                 raise ValueError(f"{n} is missing")
-            if not _fits(t, torch.float32, (M,)):
-                _dev(t, n)
-                raise ValueError(f"{n} must be float32 [{M}]")
-    p = _norm_params(dt, D, post_weight, pre_weight, gate, residual_scale, 0.0)
-    _here(dRn, dN, Y, Rn, rstd_post, rstd_pre, post_weight, pre_weight, gate)
+            if not _fits(t, dev, torch.float32, (M,)):
+                _refuse(t, n, f"float32 [{M}]")
+    p = _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, 0.0)
     dY = torch.empty_like(Y)
     dR = torch.empty_like(Y)
     dw1 = torch.empty_like(post_weight) if post_weight is not None else None

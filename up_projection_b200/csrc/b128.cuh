@@ -6,6 +6,7 @@
 
 #include "activation.cuh"
 #include "gemm_common.cuh"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace swiglu {
@@ -34,14 +35,6 @@ struct Out {
     int act;
     float alpha;
 };
-
-__device__ __forceinline__ void griddep_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void griddep_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // mbar_wait for waits that are long by design: after one test the thread
 // sleeps until the phase completes (or 20 us have passed) instead of polling,

@@ -20,8 +20,8 @@
 
 #include <atomic>
 
-#include "b128.cuh"
 #include "kernels.cuh"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace swiglu {
@@ -32,8 +32,6 @@ __device__ unsigned int g_block_norm_status;
 namespace {
 
 using namespace dev;
-using b128::griddep_launch_dependents;
-using b128::griddep_wait;
 
 constexpr int kRowThreadsMax = 512;
 constexpr int kBlockThreads = 256;  // row groups fill a block up to this
@@ -182,6 +180,8 @@ __global__ void __launch_bounds__(kRowThreadsMax) block_norm_kernel(const NormAr
     const int nvec = a.D / kE;
     const float inv_d = 1.0f / static_cast<float>(a.D);
     int turn = 0;
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + grp; row < a.M;
          row += stride) {
@@ -315,6 +315,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
     }
     if (threadIdx.x == 0) abort_flag = 0;
     __syncthreads();
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t row0 = a.M * blockIdx.x / gridDim.x + grp, row1 = a.M * (blockIdx.x + 1) / gridDim.x;
     auto copy_row = [&](int64_t row, int to) {
         const uint32_t fb = full + 8 * to, st = ring + to * 2u * pitch;
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_bwd_kernel(const N
     }
     if (threadIdx.x == 0) abort_flag = 0;
     __syncthreads();
+    griddep_wait();
     const int64_t items = a.gates * a.splits;
     auto rows_of = [&](int64_t item, int64_t &row0, int64_t &row1) {
         const int64_t gr = item / a.splits, sp = item - gr * a.splits;
@@ -818,6 +821,7 @@ __global__ void __launch_bounds__(32 * kReduceRows) block_norm_reduce_kernel(con
     const bool gates = blockIdx.y > 0;
     const int64_t gr = static_cast<int64_t>(blockIdx.y) - 1;
     float v0 = 0.0f, v1 = 0.0f;
+    griddep_launch_dependents();
     griddep_wait();
     if (col < a.D) {
         if (gates) {
@@ -945,8 +949,8 @@ cudaError_t launch_fwd_ring(const NormArgs &a, const RingShape &s, const DeviceI
     const uint32_t row = 2u * 16u * s.v * s.T;
     int stages = static_cast<int>(kRingRoom / (row * s.groups));
     if (stages > kMaxRing) stages = kMaxRing;
-    kernel<<<dev.sm_count, s.T * s.groups, stages * row * s.groups, stream>>>(a, s.T, s.groups, stages);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dev.sm_count, s.T * s.groups, stages * row * s.groups, stream, a, s.T, s.groups,
+                            stages);
 }
 
 template <bool kBf16, int kV>
@@ -954,8 +958,8 @@ cudaError_t launch_fwd_v(const NormArgs &a, const RowShape &s, int sm_count, cud
     int64_t blocks = (a.M + s.groups - 1) / s.groups;
     const int64_t most = static_cast<int64_t>(sm_count) * (2048 / (s.T * s.groups));
     if (blocks > most) blocks = most;
-    block_norm_kernel<kBf16, kV><<<static_cast<unsigned>(blocks), dim3(s.T, s.groups), 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(block_norm_kernel<kBf16, kV>, static_cast<unsigned>(blocks), dim3(s.T, s.groups), 0, stream,
+                            a);
 }
 
 template <bool kBf16>
@@ -983,8 +987,7 @@ cudaError_t launch_bwd_v(const NormBwdArgs &a, const BwdPlan &p, const DeviceInf
     auto kernel = block_norm_bwd_kernel<kBf16, kV, kGates>;
     const cudaError_t e = opt_in(kernel, mask, dev);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(p.blocks), p.T * p.groups, p.smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, static_cast<unsigned>(p.blocks), p.T * p.groups, p.smem, stream, a);
 }
 
 template <bool kGates>
@@ -1085,17 +1088,8 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
     r.scale = n.scale;
     const dim3 grid((D + 31) / 32, static_cast<unsigned>(1 + (a.accg ? gates : 0)));
     const dim3 block(32, kReduceRows);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return f32 ? cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel<false>, r)
-               : cudaLaunchKernelEx(&cfg, block_norm_reduce_kernel<true>, r);
+    return f32 ? launch_dependent(block_norm_reduce_kernel<false>, grid, block, 0, stream, r)
+               : launch_dependent(block_norm_reduce_kernel<true>, grid, block, 0, stream, r);
 }
 
 cudaError_t block_norm_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {

@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // arrive or MMA that reaches the other CTA
     cluster_sync_all();
     tc_fence_after();
+    griddep_launch_dependents();
+    griddep_wait();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_ptr);
 
     // tile t: the CTA's rows m0 .., the tile's groups g0 .. g0 + cnt of 32 columns
@@ -563,35 +565,38 @@ PairPlan make_pair_plan(int M, int N, int K, bool gated, bool row_scales, int pa
     return p;
 }
 
-std::atomic<unsigned> g_pair_attr_set_mask[3];
+std::atomic<int> g_pair_clusters[3][32];   // per mode and device, 0: not asked yet
 
 template <int kMode>
 cudaError_t launch_pair(const void *A, const float *As, const void *B0, const float *Bs0,
                         const void *B1, const float *Bs1, const Out &out, int M, int N, int K,
                         const DeviceInfo &dev, cudaStream_t stream) {
     auto kernel = swiglu_gemm_b128_pair_kernel<kMode>;
-    const unsigned bit = 1u << (dev.device & 31);
-    if (!(g_pair_attr_set_mask[kMode].load() & bit)) {
-        cudaError_t e = prepare_kernel(kernel, PairLayout<kMode>::kSmem);
-        if (e != cudaSuccess) return e;
-        g_pair_attr_set_mask[kMode].fetch_or(bit);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = PairLayout<kMode>::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(2);
-    int max_clusters = 0;
-    cudaError_t e = cudaOccupancyMaxActiveClusters(&max_clusters, kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    if (max_clusters < 1) return cudaErrorInvalidConfiguration;
+    cudaError_t e;
+    int max_clusters = g_pair_clusters[kMode][dev.device & 31].load();
+    if (max_clusters == 0) {
+        e = prepare_kernel(kernel, PairLayout<kMode>::kSmem);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(2);
+        e = cudaOccupancyMaxActiveClusters(&max_clusters, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (max_clusters < 1) return cudaErrorInvalidConfiguration;
+        g_pair_clusters[kMode][dev.device & 31].store(max_clusters);
+    }
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     const PairPlan p = make_pair_plan(M, N, K, kMode == kGated, kMode == kRowScales, max_clusters);
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "kernels.cuh"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace swiglu {
@@ -97,6 +98,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const void *__rest
     const unsigned across = (cb + kRowBlocks - 1) / kRowBlocks;
     const int64_t row = static_cast<int64_t>(blockIdx.x / across) * kRowsPerBlock + (threadIdx.x >> 4);
     const int b0 = static_cast<int>(blockIdx.x % across) * kRowBlocks;
+    griddep_launch_dependents();
+    griddep_wait();
     Oct<kBf16> x[kRowBlocks];
 #pragma unroll
     for (int j = 0; j < kRowBlocks; ++j) {
@@ -140,6 +143,8 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const void *__rest
     const int tc = static_cast<int>(blockIdx.x % across);
     const int64_t r0 = tr * 128 + 8 * h;
     const int c0 = tc * 128 + 8 * lane;
+    griddep_launch_dependents();
+    griddep_wait();
     Oct<kBf16> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -230,29 +235,27 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const void *__rest
 }
 
 template <bool kBf16>
-void launch(const void *X, uint8_t *Q, float *S, int64_t R, int C, bool tile, bool trans,
+cudaError_t launch(const void *X, uint8_t *Q, float *S, int64_t R, int C, bool tile, bool trans,
             cudaStream_t stream) {
     const int cb = (C + 127) / 128;
     if (!tile && !trans) {
         const unsigned grid = static_cast<unsigned>((cb + kRowBlocks - 1) / kRowBlocks *
                                                     ((R + kRowsPerBlock - 1) / kRowsPerBlock));
-        quant_rows_kernel<kBf16><<<grid, kThreads, 0, stream>>>(X, Q, S, R, C, (R + 3) / 4 * 4);
-        return;
+        return launch_dependent(quant_rows_kernel<kBf16>, grid, kThreads, 0, stream, X, Q, S, R, C, (R + 3) / 4 * 4);
     }
     const unsigned grid = static_cast<unsigned>(cb * ((R + 127) / 128));
     const int64_t Rp = (R + 15) / 16 * 16;
-    if (!trans) quant_tile_kernel<kBf16, true, false><<<grid, kThreads, 0, stream>>>(X, Q, S, R, C, Rp);
-    else if (tile) quant_tile_kernel<kBf16, true, true><<<grid, kThreads, 0, stream>>>(X, Q, S, R, C, Rp);
-    else quant_tile_kernel<kBf16, false, true><<<grid, kThreads, 0, stream>>>(X, Q, S, R, C, Rp);
+    if (!trans) return launch_dependent(quant_tile_kernel<kBf16, true, false>, grid, kThreads, 0, stream, X, Q, S, R, C, Rp);
+    if (tile) return launch_dependent(quant_tile_kernel<kBf16, true, true>, grid, kThreads, 0, stream, X, Q, S, R, C, Rp);
+    return launch_dependent(quant_tile_kernel<kBf16, false, true>, grid, kThreads, 0, stream, X, Q, S, R, C, Rp);
 }
 
 }  // namespace
 
 cudaError_t launch_quant_b128(const void *X, void *Q, float *S, int64_t R, int C, int f32,
                               bool tile, bool trans, cudaStream_t stream) {
-    if (f32) launch<false>(X, static_cast<uint8_t *>(Q), S, R, C, tile, trans, stream);
-    else launch<true>(X, static_cast<uint8_t *>(Q), S, R, C, tile, trans, stream);
-    return cudaGetLastError();
+    return f32 ? launch<false>(X, static_cast<uint8_t *>(Q), S, R, C, tile, trans, stream)
+               : launch<true>(X, static_cast<uint8_t *>(Q), S, R, C, tile, trans, stream);
 }
 
 }  // namespace swiglu
