@@ -601,3 +601,152 @@ def test_mlp_block_forward_and_backward():
     plain = dy.double() @ Wd.double()
     assert float((dH.double() - plain).norm() / plain.norm()) < 2.0 ** -3
     assert bool(torch.isfinite(dG).all()) and bool(torch.isfinite(dU).all())
+
+
+# ------------------------------------------------ many rows, calls in flight
+
+@pytest.mark.parametrize("dtype,M,D", [("bf16", 1300, 4096), ("bf16", 1185, 4104), ("bf16", 700, 8192),
+                                       ("f32", 605, 5120), ("f32", 2370, 2052), ("f32", 600, 8192)])
+@pytest.mark.parametrize("post,pre,gate", [(True, True, "channel"), (False, True, "groups"),
+                                           (True, False, "rows"), (False, False, "none")])
+def test_norm_many_rows_matches_fp64(dtype, M, D, post, pre, gate):
+    """Rows of 8 KB and more, several per block: rows through shared memory."""
+    v = norm_inputs(M, D, dtype, post, pre, gate_count(M, gate), M + D)
+    s, eps = 0.7, 1e-6
+    Rn, N, r1, r2 = up.swiglu_block_norm(v["Y"], v["R"], v["post"], v["pre"], v["gate"], residual_scale=s,
+                                         eps=eps, return_stats=True)
+    wRn, wN, w1, w2, mag = ref.norm_fwd(v["Y"], v["R"], v["post"], v["pre"], v["gate"], s, eps)
+    stat = (32 + 5 + 16 + 8) * U24   # as in test_norm_matches_fp64
+    h = HALF[DT[dtype]]
+    within(Rn, wRn, h * wRn.abs() + (stat + 8 * U24) * (1 + h) * mag, "Rn")
+    if post:
+        within(r1, w1, stat * w1, "rstd_post")
+    if pre:
+        off = (stat + 8 * U24) * (mag * mag).mean(1).sqrt() * w2
+        within(r2, w2, (stat + off) * w2, "rstd_pre")
+        m = v["pre"].double().abs() * mag * w2[:, None]
+        within(N, wN, h * wN.abs() + (1 + h) * ((stat + 8 * U24) * m + (stat + off)[:, None] * wN.abs()), "N")
+
+
+def test_norm_many_rows_in_place_and_non_finite():
+    M, D = 1300, 4096
+    v = norm_inputs(M, D, "bf16", True, True, 1)
+    want, wn = up.swiglu_block_norm(v["Y"], v["R"], v["post"], v["pre"], v["gate"])
+    bad = [0, 7, 649, 1299]
+    Y = v["Y"].clone()
+    Y[bad, 5] = torch.tensor([float("inf"), float("nan"), float("-inf"), float("nan")], dtype=torch.bfloat16,
+                             device=dev())
+    R = v["R"].clone()
+    Rn, N = up.swiglu_block_norm(Y, R, v["post"], v["pre"], v["gate"], Rn=R)
+    synced()
+    good = torch.ones(M, dtype=torch.bool, device=dev())
+    good[bad] = False
+    assert Rn is R and torch.equal(Rn[good], want[good]) and torch.equal(N[good], wn[good])
+    assert bool(torch.isnan(N[~good]).any(1).all())
+
+
+@pytest.mark.parametrize("dtype,M,D,groups", [("bf16", 700, 8192, 1), ("bf16", 640, 8192, 10), ("bf16", 320, 16384, 1),
+                                              ("bf16", 320, 16384, 2), ("bf16", 400, 12008, 0), ("bf16", 5000, 64, 5),
+                                              ("bf16", 6000, 256, 1), ("f32", 500, 8188, 1), ("f32", 480, 8192, 3),
+                                              ("f32", 1020, 1536, 12), ("f32", 4500, 16, 4500)])
+def test_norm_bwd_row_lengths(dtype, M, D, groups):
+    """The layouts of the row rings: one warp to 16 per row, 8 to 32 elements
+    per thread, one stage to many."""
+    check_bwd(norm_inputs(M, D, dtype, True, True, groups, M + D), dtype, M, D, M + 1)
+
+
+def test_norm_bwd_non_finite_row_stays_in_its_row():
+    M, D = 600, 4096
+    v = norm_inputs(M, D, "bf16", True, True, 1)
+    Rn, _, r1, r2 = up.swiglu_block_norm(v["Y"], v["R"], v["post"], v["pre"], v["gate"], return_stats=True)
+    dRn, dN = rand((M, D), 5, torch.bfloat16), rand((M, D), 6, torch.bfloat16)
+    want = run_bwd(v, r1, r2, Rn, dRn, dN, 1.0)
+    bad = dN.clone()
+    bad[[3, 599], 9] = float("inf")
+    got = run_bwd(v, r1, r2, Rn, dRn, bad, 1.0)
+    synced()
+    good = torch.ones(M, dtype=torch.bool, device=dev())
+    good[[3, 599]] = False
+    for k in ("dY", "dR"):
+        assert torch.equal(got[k][good], want[k][good])
+    assert not bool(torch.isfinite(got["d_pre"][9])) and bool(torch.isfinite(got["d_pre"][10:]).all())
+
+
+def mlp_step(x, res, w1, w2, Wg, Wu, Wd):
+    """norm, gate and up, down, norm, all operands quantised on the way."""
+    r0, n0 = up.swiglu_block_norm(x, res, None, w2)
+    nq, ns = up.swiglu_quant_b128(n0)
+    (gq, gs), (uq, us), (dq, ds) = (up.swiglu_quant_b128(w, block="tile") for w in (Wg, Wu, Wd))
+    hq, hs = up.swiglu_quant_b128(up.swiglu_fwd_b128(nq, ns, gq, gs, uq, us))
+    return up.swiglu_block_norm(up.swiglu_gemm_b128(hq, hs, dq, ds), r0, w1, w2, residual_scale=0.5)
+
+
+def mlp_weights(D, F, seed):
+    bf = torch.bfloat16
+    return (rand((D,), seed + 3, bf, 0.1, 1.0), rand((D,), seed + 4, bf, 0.1, 1.0),
+            rand((F, D), seed + 5, bf, D ** -0.5), rand((F, D), seed + 6, bf, D ** -0.5),
+            rand((D, F), seed + 7, bf, F ** -0.5))
+
+
+@pytest.mark.parametrize("M", [1, 8, 60, 200])
+def test_steps_in_flight_keep_their_order(M):
+    """Each kernel starts while the one before it drains; weights and
+    activations are written by the kernels just before.  Steps without a wait
+    between them, memory of one reused by the next, give the bits of steps
+    that are waited for."""
+    D, F = 512, 1040
+    bf = torch.bfloat16
+    steps = [(rand((M, D), 30 + i, bf, 0.5), rand((M, D), 60 + i, bf, 2.0), mlp_weights(D, F, 100 * i))
+             for i in range(4)]
+    want = []
+    for x, res, w in steps:
+        want.append(mlp_step(x, res, *w))
+        synced()
+    for _ in range(5):
+        got = [mlp_step(x, res, *w) for x, res, w in steps]
+        for g, t in zip(got, want):
+            assert torch.equal(g[0], t[0]) and torch.equal(g[1], t[1])
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_step_captured_and_on_two_streams(M):
+    D, F = 512, 1040
+    bf = torch.bfloat16
+    w = mlp_weights(D, F, 0)
+    a, b = ((rand((M, D), 30 + i, bf, 0.5), rand((M, D), 60 + i, bf, 2.0)) for i in range(2))
+    want = [mlp_step(*a, *w), mlp_step(*b, *w)]
+    synced()
+    # two streams at once
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s, v in zip(side, (a, b)):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([mlp_step(*v, *w) for _ in range(10)])
+    torch.cuda.synchronize()
+    for t, all_ in zip(want, got):
+        for g in all_:
+            assert torch.equal(g[0], t[0]) and torch.equal(g[1], t[1])
+    # two graphs, replayed in turn and side by side
+    graphs, outs, ins = [], [], []
+    for v in (a, b):
+        x, res = torch.zeros_like(v[0]), torch.zeros_like(v[1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(mlp_step(x, res, *w))
+        graphs.append(g)
+        ins.append((x, res))
+    for (x, res), v in zip(ins, (a, b)):
+        x.copy_(v[0])
+        res.copy_(v[1])
+    torch.cuda.synchronize()
+    for rounds in range(3):
+        for s, g in zip(side, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for g, t in zip(outs, want):
+            assert torch.equal(g[0], t[0]) and torch.equal(g[1], t[1])
+            g[0].zero_()
+            g[1].zero_()
+        torch.cuda.synchronize()
