@@ -117,6 +117,52 @@ __device__ __forceinline__ void mma_commit_own(uint32_t bar) {
         : "memory");
 }
 
+// 16 lanes x 32 columns of TMEM as fragments: registers 4 j .. + 3 hold columns
+// 8 j + 2 (lane mod 4), + 1 of rows lane / 4 and lane / 4 + 8.
+template <int kAt>
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[kAt]), "=r"(r[kAt + 1]), "=r"(r[kAt + 2]), "=r"(r[kAt + 3]), "=r"(r[kAt + 4]),
+          "=r"(r[kAt + 5]), "=r"(r[kAt + 6]), "=r"(r[kAt + 7]), "=r"(r[kAt + 8]), "=r"(r[kAt + 9]),
+          "=r"(r[kAt + 10]), "=r"(r[kAt + 11]), "=r"(r[kAt + 12]), "=r"(r[kAt + 13]), "=r"(r[kAt + 14]),
+          "=r"(r[kAt + 15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts_b64(uint32_t addr, unsigned long long v) {
+    asm volatile("st.shared.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// A block's 32 columns of a warp's 32 rows into its running sums, with row
+// scales.  A lane that holds a whole row needs all 32 of B's scales, 512 bytes
+// a warp for every 128-byte broadcast; as fragments (sums 8 h + 2 j + i: rows
+// 16 h + 8 i + lane / 4, columns 8 j + 2 (lane mod 4), + 1) it needs 8 of them
+// and four of A's.  sb: the scales of this lane's first two columns.
+__device__ __forceinline__ void add_fragments(unsigned long long (&acc)[16], const uint32_t (&v)[32],
+                                              const float (&sa)[4], uint32_t sb) {
+    unsigned long long sa2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sa2[i] = pair2(sa[i], sa[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        unsigned long long w;
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w) : "r"(sb + 32u * j));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                fma2(acc[8 * h + 2 * j + i], v[16 * h + 4 * j + 2 * i], v[16 * h + 4 * j + 2 * i + 1],
+                     mul2(w, sa2[2 * h + i]));
+    }
+}
+
 // tm_b: rows of B (gated: of Wg), tm_u: of Wu, boxes of half_rows rows.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -354,24 +400,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[j][i] = 0ull;
-            float sa = 0.0f, sb[4] = {};
+            constexpr bool kFrag = kMode == kRowScales;
+            float sa[kFrag ? 4 : 1] = {}, sb[4] = {};
             uint32_t srow = 0;        // this block's row scales of B
             uint32_t v[2][32];
+            auto read_group = [&](uint32_t at, uint32_t (&r)[32]) {
+                if constexpr (kFrag) {
+                    tmem_ld_16x256b_x4<0>(at, r);
+                    tmem_ld_16x256b_x4<16>(at + (16u << 16), r);
+                } else {
+                    tmem_ld_32x32b_x32(at, r);
+                }
+            };
             // One block ahead: wait for its accumulators, start reading them,
             // and fetch its scales.
             auto open_block = [&](bool new_slot) -> bool {
                 if (new_slot) {
                     if (!mbar_wait_long(bar_sfull + 8 * slot, sphase, abort_flag)) return false;
-                    pa = base + L::kOffSlots + slot * L::kSlotBytes + 4u * (quad * 32 + lane);
-                    pb = base + L::kOffSlots + slot * L::kSlotBytes + L::kOffB + (kMode == kRowScales ? 0u : 16u * half);
+                    pa = base + L::kOffSlots + slot * L::kSlotBytes + 4u * (quad * 32 + (kFrag ? lane >> 2 : lane));
+                    pb = base + L::kOffSlots + slot * L::kSlotBytes + L::kOffB + (kFrag ? 8u * (lane & 3) : 16u * half);
                 }
                 if (!mbar_wait_long(bar_tfull + buf8, bphase, abort_flag)) return false;
                 tc_fence_after();
                 if (groups == 0) return true;
-                tmem_ld_32x32b_x32(lanes + 32u * buf8 + col0, v[0]);
-                sa = lds_f32(pa);
+                read_group(lanes + 32u * buf8 + col0, v[0]);
+#pragma unroll
+                for (int i = 0; i < (kFrag ? 4 : 1); ++i) sa[i] = lds_f32(pa + 32u * i);
                 pa += 512u;
-                if constexpr (kMode != kRowScales) {
+                if constexpr (!kFrag) {
                     const uint4 w = lds_v4(pb);
                     pb += 32u;
                     sb[0] = __uint_as_float(w.x);
@@ -392,15 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = lanes + 32u * buf8;
                 float s[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] = sa * sb[j];
-                const float sa_now = sa;
+                for (int j = 0; j < 4; ++j) s[j] = sa[0] * sb[j];
+                float sa_now[kFrag ? 4 : 1];
+#pragma unroll
+                for (int i = 0; i < (kFrag ? 4 : 1); ++i) sa_now[i] = sa[i];
                 const uint32_t srow_now = srow;
-                auto read = [&](int o) {
-                    tmem_ld_32x32b_x32(d + (o < 2 ? col0 : col2) + 32u * (o & 1), v[o & 1]);
-                };
+                auto read = [&](int o) { read_group(d + (o < 2 ? col0 : col2) + 32u * (o & 1), v[o & 1]); };
                 auto add = [&](int o) {
-                    if constexpr (kMode == kRowScales)
-                        add_rows(acc[o], v[o & 1], sa_now, srow_now + 4u * ((o < 2 ? col0 : col2) + 32u * (o & 1)));
+                    if constexpr (kFrag)
+                        add_fragments(acc[o], v[o & 1], sa_now, srow_now + 4u * ((o < 2 ? col0 : col2) + 32u * (o & 1)));
                     else
                         add_block(acc[o], v[o & 1], s[o]);
                 };
@@ -451,10 +507,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t box = obuf + static_cast<uint32_t>(onext) * 2048u;
                 if (lane == 0) bulk_wait_read<3>();  // the store from this box four boxes ago
                 __syncwarp();
+                if constexpr (kFrag) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    sts_v4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
-                           make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3)));
+                    for (int i = 0; i < 16; ++i) {   // sum i: see add_fragments
+                        const int r = 16 * (i >> 3) + 8 * (i & 1) + (lane >> 2), j = (i >> 1) & 3;
+                        sts_b32(box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4) + 4 * (lane & 3), value(i));
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts_v4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
+                               make_uint4(value(4 * c), value(4 * c + 1), value(4 * c + 2), value(4 * c + 3)));
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -500,12 +564,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t box = obuf + static_cast<uint32_t>(onext & 1) * 4096u;
                         if (lane == 0) bulk_wait_read<1>();  // the store from this box two boxes ago
                         __syncwarp();
+                        if constexpr (kFrag) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const unsigned long long a0 = acc[j][2 * c], a1 = acc[j][2 * c + 1];
-                            sts_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4),
-                                   make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
-                                              static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32)));
+                            for (int i = 0; i < 16; ++i) {
+                                const int r = 16 * (i >> 3) + 8 * (i & 1) + (lane >> 2);
+                                const int c = (i & 6) + ((lane >> 1) & 1);
+                                sts_b64(box + r * 128 + ((c ^ (r & 7)) << 4) + 8 * (lane & 1), acc[j][i]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const unsigned long long a0 = acc[j][2 * c], a1 = acc[j][2 * c + 1];
+                                sts_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4),
+                                       make_uint4(static_cast<uint32_t>(a0), static_cast<uint32_t>(a0 >> 32),
+                                                  static_cast<uint32_t>(a1), static_cast<uint32_t>(a1 >> 32)));
+                            }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
