@@ -1,5 +1,5 @@
 // gemm_b128_plan_check.cu -- host-only check of the block-scaled products'
-// tiles for M > 128 (the kernel is compiled with the translation unit, never
+// tiles for M > 32 (the kernel is compiled with the translation unit, never
 // launched): tiles cover the columns, TMA boxes within 256, the MMA's N legal
 // and inside a TMEM buffer, every group's columns inside it.
 // Prints "ok <plans checked>" or the first violation.
@@ -52,7 +52,7 @@ int check(int M, int N, int K, int mode, int pairs) {
 
 int main() {
     long checked = 0;
-    const int Ms[] = {129, 256, 257, 300, 1000, 2048, 4097, 8192, 100000};
+    const int Ms[] = {33, 64, 65, 128, 129, 256, 257, 300, 1000, 2048, 4097, 8192, 100000};
     const int Ks[] = {16, 128, 144, 1536, 14336, 1 << 20};
     for (int pairs : {1, 4, 66, 72, 74, 80})
         for (int mode = 0; mode < 3; ++mode)

@@ -1,5 +1,5 @@
 // gemm_b128_stream_plan_check.cu -- host-only check of the block-scaled
-// products' plans for M <= 128 (the kernel is compiled with the translation
+// products' plans for M <= 64 (the kernel is compiled with the translation
 // unit, never launched): shared memory within the opt-in limit, ring regions
 // disjoint and aligned, the MMA's reads past a tile's rows and the exchange of
 // sums inside the allocation, TMA boxes within 256, the MMA's N and the TMEM
@@ -35,7 +35,7 @@ int check(int M, int N, int K, int mode, int sms) {
     if (p.a_rows < M || p.a_rows % 8 || p.a_rows > 128 || p.mma_n < M || p.mma_n % 16 || p.mma_n > 128)
         return fail("rows of A", M, N, K, mode, sms);
     const int hi = p.units % p.tiles ? p.q + 1 : p.q;
-    if (p.rows != 8 * sides * hi || p.rows > (p.tok == 64 ? 128 : 256) || (p.mma_m != 64 && p.mma_m != 128) || (p.mma_m == 64 && p.nrt != 1) ||
+    if (p.rows != 8 * sides * hi || p.rows > 256 || (p.mma_m != 64 && p.mma_m != 128) || (p.mma_m == 64 && p.nrt != 1) ||
         p.nrt != (p.rows + p.mma_m - 1) / p.mma_m)
         return fail("weight rows", M, N, K, mode, sms);
     if (p.kbs > 8 || 4 * p.kbs > 32) return fail("TMA box", M, N, K, mode, sms);
@@ -96,7 +96,7 @@ int check(int M, int N, int K, int mode, int sms) {
 
 int main() {
     long checked = 0;
-    const int Ms[] = {1, 7, 8, 9, 16, 17, 32, 33, 64, 65, 72, 96, 100, 127, 128};
+    const int Ms[] = {1, 7, 8, 9, 16, 17, 24, 31, 32, 33, 40, 48, 63, 64};
     const int Ks[] = {16, 128, 144, 256, 400, 1024, 1536, 2000, 4096, 14336, 1 << 20};
     for (int sms : {2, 16, 132, 148, 160})
         for (int mode = 0; mode < 3; ++mode)
@@ -107,7 +107,7 @@ int main() {
                         ++checked;
                     }
     for (int mode = 0; mode < 3; ++mode)
-        if (check(128, 1 << 20, 4096, mode, 148)) return 1;
+        if (check(64, 1 << 20, 4096, mode, 148)) return 1;
     std::printf("ok %ld\n", checked);
     return 0;
 }

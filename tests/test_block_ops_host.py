@@ -19,7 +19,7 @@ NULL, DIM, MDIM, MPTR, DTYPE, OVER, EPI, BLOCK = (
 
 def test_product_plans_keep_memory_bounds():
     """Shared memory, TMA boxes, TMEM columns and tiles of the block-scaled
-    products' plans, M > 128 and M <= 128 (gemm_b128_plan_check.cu,
+    products' plans, many rows and few (gemm_b128_plan_check.cu,
     gemm_b128_stream_plan_check.cu)."""
     csrc = "up_projection_b200/csrc/"
     _build_and_run(["tests/gemm_b128_plan_check.cu", csrc + "gemm_b128_stream.cu", csrc + "tmap.cu"], 100000)

@@ -750,3 +750,21 @@ def test_step_captured_and_on_two_streams(M):
             g[0].zero_()
             g[1].zero_()
         torch.cuda.synchronize()
+
+
+# Row counts around the change of kernels (32 and 64 rows), short and long
+# reductions.
+TURNS = [(m, 520, k) for m in (31, 32, 33, 63, 64, 65) for k in (2032, 2048, 2064, 2192)] + [(64, 8, 14336),
+                                                                                              (40, 20000, 2176)]
+
+
+@pytest.mark.parametrize("block", ["tile", "row"])
+@pytest.mark.parametrize("M,N,K", TURNS)
+def test_gemm_row_counts_are_exact(M, N, K, block):
+    test_gemm_integers_are_exact(M, N, K, block)
+
+
+@pytest.mark.parametrize("order", ["gate first", "up first", "one weight"])
+@pytest.mark.parametrize("M,K", [(33, 2192), (60, 2176), (64, 2192), (65, 2192), (128, 384)])
+def test_gated_row_counts_are_exact(M, K, order):
+    test_gated_weights_in_any_place(M, K, order)

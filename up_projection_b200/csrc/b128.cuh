@@ -1,5 +1,5 @@
 // b128.cuh -- pieces shared by the two kernels of the block-scaled e4m3
-// products (gemm_b128.cu: large M; gemm_b128_stream.cu: M <= 128).
+// products (gemm_b128.cu: large M; gemm_b128_stream.cu: few rows).
 #pragma once
 
 #include <cuda_bf16.h>

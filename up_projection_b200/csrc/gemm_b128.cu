@@ -5,7 +5,7 @@
 //
 // with Bs one value per row of B ("row") or per 128 rows ("tile"); and the
 // gated pair, H = act(alpha G) * U with G and U such products of one A.  This
-// file: M > 128 (gemm_b128_stream.cu: M <= 128).
+// file: all but the few rows (b128_few_rows) of gemm_b128_stream.cu.
 //
 // The scales differ from block to block, so the tensor cores accumulate one
 // 128-deep block only: four MMAs (K = 32) into one of two buffers of tensor
@@ -714,7 +714,7 @@ cudaError_t launch_pair(const void *A, const float *As, const void *B0, const fl
 cudaError_t launch_gemm_b128(const void *A, const float *As, const void *B, const float *Bs,
                              void *Y, int M, int N, int K, bool row_scales, int f32_out,
                              const DeviceInfo &dev, cudaStream_t stream) {
-    if (M <= kB128StreamMaxM)
+    if (b128_few_rows(M, K))
         return launch_gemm_b128_stream(A, As, B, Bs, Y, M, N, K, row_scales, f32_out, dev, stream);
     Out out{};
     out.y = Y;
@@ -726,7 +726,7 @@ cudaError_t launch_gemm_b128(const void *A, const float *As, const void *B, cons
 cudaError_t launch_fwd_b128(const void *X, const float *Xs, const void *Wg, const float *Gs,
                             const void *Wu, const float *Us, void *H, int M, int N, int K,
                             const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream) {
-    if (M <= kB128StreamMaxM)
+    if (b128_few_rows(M, K))
         return launch_fwd_b128_stream(X, Xs, Wg, Gs, Wu, Us, H, M, N, K, epi, dev, stream);
     Out out{};
     out.y = H;

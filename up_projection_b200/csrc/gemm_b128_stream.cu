@@ -1,5 +1,5 @@
 // gemm_b128_stream.cu -- the block-scaled e4m3 products (gemm_b128.cu) for
-// M <= 128 rows of A: a read of the weights from HBM once, on the fp8 tensor
+// M <= 64 rows of A (b128_few_rows): a read of the weights from HBM once, on the fp8 tensor
 // cores.
 //
 // The operands are swapped against the large products: the weights are the
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    const float *__restrict__ bs0, const float *__restrict__ bs1,
                                    const Out out, int M, int N, int num_kb, int joined, int swapped,
                                    const StreamPlan p) {
-    constexpr int kRt = kTok == 64 ? 1 : 2;   // groups of 128 rows a warp can hold
+    constexpr int kRt = 2;   // groups of 128 rows a warp can hold
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const int b1 = work ? min(nb, b0 + p.g) : 0;
                     // kBatch blocks' reads are in flight together
-                    constexpr int kBatch = kTok == 8 ? 4 : (kTok == 32 ? 2 : 1);
+                    constexpr int kBatch = kTok == 8 ? 4 : 2;
                     const int next = p.parity ? 2 : 1;
                     for (int b = b0 + (p.parity ? half : 0); b < b1; b += kBatch * next) {
 #pragma unroll
@@ -394,9 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if constexpr (kTok == 8) {
                                         tmem_ld_32x32b_x8(d, v[q]);
                                     } else {
-#pragma unroll
-                                        for (int j = 0; j < kTok / 32; ++j)
-                                            tmem_ld_32x32b_x32(d + 32u * j, *reinterpret_cast<uint32_t(*)[32]>(&v[q][32 * j]));
+                                        tmem_ld_32x32b_x32(d, v[q]);
                                     }
                                     f[q] = lds_f32(sb_src + static_cast<uint32_t>(bq) * b_step + at[rt]);
                                 }
@@ -414,13 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         fma2(acc[rt][2], v[q][4], v[q][5], mul2(pair2(__uint_as_float(w1.x), __uint_as_float(w1.y)), s2));
                                         fma2(acc[rt][3], v[q][6], v[q][7], mul2(pair2(__uint_as_float(w1.z), __uint_as_float(w1.w)), s2));
                                     } else {
-#pragma unroll
-                                        for (int j = 0; j < kTok / 32; ++j) {
-                                            uint32_t(&vj)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[q][32 * j]);
-                                            tmem_ld_wait(vj);
-                                            add_rows(*reinterpret_cast<unsigned long long(*)[16]>(&acc[rt][16 * j]), vj, f[q],
-                                                     sa + 128u * j);
-                                        }
+                                        tmem_ld_wait(v[q]);
+                                        add_rows(acc[rt], v[q], f[q], sa);
                                     }
                                 }
                             }
@@ -562,10 +555,10 @@ StreamPlan make_stream_plan(int M, int N, int K, bool gated, bool row_scales, co
         p.full = K / kBlockK;
         p.a_rows = (M + 7) / 8 * 8;
         p.mma_n = (M + 15) / 16 * 16;
-        p.tok = M <= 8 ? 8 : (M <= 64 ? 32 : 64);
+        p.tok = M <= 8 ? 8 : 32;
         p.parity = M <= 32 ? 1 : 0;
         p.part_m = p.parity ? p.a_rows : 2 * p.tok;
-        const int max_units = (p.tok == 64 ? 128 : 256) / (8 * sides);
+        const int max_units = 256 / (8 * sides);
         const int least = (p.units + max_units - 1) / max_units;
         p.tiles = p.units < max_clusters[ci] ? p.units : max_clusters[ci];
         if (p.tiles < least) p.tiles = least;
@@ -574,7 +567,7 @@ StreamPlan make_stream_plan(int M, int N, int K, bool gated, bool row_scales, co
         p.rows = 8 * sides * cnt;
         p.mma_m = p.rows <= 64 ? 64 : 128;
         p.nrt = (p.rows + p.mma_m - 1) / p.mma_m;
-        p.acc_cols = p.tok == 8 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+        p.acc_cols = p.tok == 8 ? 16 : (M <= 32 ? 32 : 64);
         p.g = 8;
         while (p.g > 1 && p.g * p.nrt * p.acc_cols > static_cast<int>(kBufCols)) p.g /= 2;
         const uint32_t exchange = 4u * static_cast<uint32_t>(c * (p.parity ? 2 : 1) * p.part_m * p.rows);
@@ -620,7 +613,7 @@ struct DeviceState {
 };
 
 std::mutex g_state_mutex;
-DeviceState g_state[3][3][64];   // mode, tok, device
+DeviceState g_state[3][2][64];   // mode, tok, device
 
 template <int kMode, int kTok>
 cudaError_t device_state(const DeviceInfo &dev, int slot, DeviceState &out) {
@@ -658,7 +651,7 @@ cudaError_t launch_stream(const void *A, const float *As, const void *B0, const 
                           const void *B1, const float *Bs1, const Out &out, int M, int N, int K,
                           const DeviceInfo &dev, cudaStream_t stream) {
     DeviceState state;
-    cudaError_t e = device_state<kMode, kTok>(dev, kTok == 8 ? 0 : (kTok == 32 ? 1 : 2), state);
+    cudaError_t e = device_state<kMode, kTok>(dev, kTok == 8 ? 0 : 1, state);
     if (e != cudaSuccess) return e;
     const StreamPlan p = make_stream_plan(M, N, K, kMode == kGated, kMode == kRowScales, state.max_clusters);
     if (p.stages < 2 || p.smem > kMaxSmem) return cudaErrorInvalidValue;
@@ -759,8 +752,7 @@ cudaError_t launch_tok(const void *A, const float *As, const void *B0, const flo
                        const float *Bs1, const Out &out, int M, int N, int K, const DeviceInfo &dev,
                        cudaStream_t stream) {
     if (M <= 8) return launch_stream<kMode, 8>(A, As, B0, Bs0, B1, Bs1, out, M, N, K, dev, stream);
-    if (M <= 64) return launch_stream<kMode, 32>(A, As, B0, Bs0, B1, Bs1, out, M, N, K, dev, stream);
-    return launch_stream<kMode, 64>(A, As, B0, Bs0, B1, Bs1, out, M, N, K, dev, stream);
+    return launch_stream<kMode, 32>(A, As, B0, Bs0, B1, Bs1, out, M, N, K, dev, stream);
 }
 
 }  // namespace

@@ -183,8 +183,15 @@ cudaError_t launch_gemm_b128(const void *A, const float *As, const void *B, cons
 cudaError_t launch_fwd_b128(const void *X, const float *Xs, const void *Wg, const float *Gs,
                             const void *Wu, const float *Us, void *H, int M, int N, int K,
                             const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream);
-// M <= 128 (gemm_b128_stream.cu), reached through the two above.
-constexpr int kB128StreamMaxM = 128;
+// Few rows (gemm_b128_stream.cu), reached through the two above.  Its time
+// grows with M, the large products' hardly does up to 256 rows; they meet
+// between 32 and 96 rows, later where the reduction is long (it is split over
+// SMs here only).  B200, both kernels, a call between two events, us: M = 96,
+// N = K = 4096 28.8 here, 20.5 there, gated 11008 x 4096 71.7 and 45.1; M = 64,
+// 4096 x 14336 36.9 and 49.2, 1024 x 1024 14.3 and 12.3, gated 6912 x 1536 22.5
+// and 18.4; M = 32, 4096 x 14336 32.8 and 47.1, gated 11008 x 4096 36.9 and 45.1.
+constexpr int kB128StreamMaxM = 64;
+inline bool b128_few_rows(int M, int K) { return M <= 32 || (M <= kB128StreamMaxM && K > 2048); }
 cudaError_t launch_gemm_b128_stream(const void *A, const float *As, const void *B, const float *Bs,
                                     void *Y, int M, int N, int K, bool row_scales, int f32_out,
                                     const DeviceInfo &dev, cudaStream_t stream);
