@@ -10,7 +10,7 @@
 // MMAs (K = 32) per block whatever M is, and lane n of the accumulator holds
 // output column n for all rows of A.  (B200, M = 8, N = 4096, K = 14336, 58.7 MB
 // of weights: A as the M operand 29.8 us; warp-level mma.sync, which unpacks
-// e4m3 to fp16 first, 22.3 us; this form 17.7 us, of 13 us that the copies alone
+// e4m3 to fp16 first, 22.3 us; this form 16.9 us, of 13 us that the copies alone
 // take.)
 //
 // A tile is R rows of weights (a multiple of 8, at most 256: two MMAs per
@@ -536,11 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Tile height, cluster and ring for `max_clusters[i]` resident clusters of
-// 2^i CTAs.  A CTA's time is the larger of its weights' share of the HBM
-// bandwidth (about 22 bytes per cycle and SM on a B200) and of its MMAs
-// (measured, per block: about 200 cycles for 128 rows, 150 for 64), and a
-// cluster costs two barriers and the exchange: the cheapest (cluster, tiles)
-// wins.
+// 2^i CTAs.  A CTA's time per block is the larger of its weights' share of the
+// HBM bandwidth (about 24 bytes per cycle and SM of the device on a B200, at
+// most 48 for one SM) and of its MMAs and
+// their accumulation (measured: 250 cycles for up to 8 rows of A, 340 up to
+// 32, 520 up to 64, per 128 rows of weights), plus some of the smaller, as they
+// do not overlap fully; a cluster costs two barriers and the exchange.  The
+// cheapest (cluster, tiles) wins.  B200, clusters of 1, 2, 4, us: M = 8, 4096 x
+// 14336 25.2, 17.7, 16.8; 512 x 4096 10.6, 8.9, 7.8; 1024 x 1024 6.5, 7.2, 6.9;
+// 11008 x 14336 31.8, 35.0, 44.5.
 StreamPlan make_stream_plan(int M, int N, int K, bool gated, bool row_scales, const int max_clusters[4]) {
     StreamPlan best{};
     long long best_cost = -1;
@@ -597,8 +601,13 @@ StreamPlan make_stream_plan(int M, int N, int K, bool gated, bool row_scales, co
         p.off_bar = p.off_slots + p.slots * p.slot_bytes;
         p.smem = p.off_bar + kTailBytes;
         const long long waves = (p.tiles + max_clusters[ci] - 1) / max_clusters[ci];
-        const long long bytes = static_cast<long long>(p.rows) * 128 / 22, mma = p.mma_m == 64 ? 150 : 200ll * p.nrt;
-        const long long cost = waves * (per_cta * (bytes > mma ? bytes : mma) + (c > 1 ? 1500 : 0));
+        const long long busy = static_cast<long long>(p.tiles < max_clusters[ci] ? p.tiles : max_clusters[ci]) * c;
+        const long long share = p.rows * 128 * busy / (24 * max_clusters[0]), alone = p.rows * 128 / 48;
+        const long long bytes = share > alone ? share : alone;
+        const long long work = p.nrt * (p.tok == 8 ? 250ll : (p.parity ? 340ll : 520ll));
+        const long long more = bytes > work ? bytes : work, less = bytes + work - more;
+        const long long cost = waves * (per_cta * (more + less * (p.nrt == 1 ? 5 : 8) / 20) +
+                                        (c > 1 ? 1200 + c * (150 + 8 * p.a_rows) : 0));
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = p;
