@@ -272,6 +272,7 @@ constexpr int kMaxRing = 8;
 constexpr int kMaxGroups = 16;   // row groups of one warp; of more, at most 8
 constexpr int kRingThreads = 512;
 constexpr uint32_t kRingRoom = 220 * 1024;
+
 // A wait of the ring that gave up: no further copies are made, and those under
 // way end before the block does.
 __device__ __noinline__ void ring_abandon(uint32_t full, int stages, int stage, uint32_t phase) {
@@ -286,7 +287,7 @@ __device__ __noinline__ void ring_abandon(uint32_t full, int stages, int stage, 
 }
 
 // The forward over runs of consecutive rows, one run per block; W1 g and W2
-// stay in registers.  M = 8192, D = 4096, bf16: 50 us, 82 % of the measured
+// stay in registers.  M = 8192, D = 4096, bf16: 49 us, 84 % of the measured
 // copy bandwidth (the two barriers of a row leave the rest).
 template <bool kBf16, int kV>
 __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const NormArgs a, const int T, const int groups,
@@ -453,7 +454,7 @@ struct NormBwdArgs {
 // fewer, e and the products of the weights (in registers); with more they are
 // formed again, because the column sums alone fill half the registers.
 // D = 4096, bf16: M = 16384 137 us with the join, 90 % of the measured copy
-// bandwidth; M = 2048 30 us, 52 % (14 rows per block: filling the rings and
+// bandwidth; M = 2048 29 us, 53 % (14 rows per block: filling the rings and
 // the join, 5 us, are a third of it).  One CTA-wide loop over rows read
 // straight from memory took 234 and 45 us: its loads waited for its barriers.
 template <bool kBf16, int kV, bool kGates>
