@@ -611,6 +611,15 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
     return (Rn, N, r1, r2) if return_stats else (Rn, N)
 
 
+def _stat(t, name, dev, M):
+    """Address of a row statistic the backward reads."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if not _fits(t, dev, torch.float32, (M,)):
+        _refuse(t, name, f"float32 [{M}]")
+    return t.data_ptr()
+
+
 def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: torch.Tensor,
                           Rn: torch.Tensor, rstd_post: torch.Tensor | None,
                           rstd_pre: torch.Tensor | None, post_weight: torch.Tensor | None = None,
@@ -623,39 +632,47 @@ def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: 
     dev, dt, code, shape, M, D = _norm_shape(Y)
     if (dN is None) != (pre_weight is None):
         raise ValueError("dN and pre_weight go together")
-    for t, n in ((Rn, "Rn"), (dRn, "dRn"), (dN, "dN")):
-        if t is not None and not _fits(t, dev, dt, shape):
-            _refuse(t, n, "of Y's dtype and shape")
-    for w, t, n in ((post_weight, rstd_post, "rstd_post"), (pre_weight, rstd_pre, "rstd_pre")):
-        if w is not None:
-            if t is None:
-                raise ValueError(f"{n} is missing")
-            if not _fits(t, dev, torch.float32, (M,)):
-                _refuse(t, n, f"float32 [{M}]")
+    pR = pN = p1 = p2 = d1 = d2 = dgp = dw1 = dw2 = dg = ws = wsp = None
+    if not _fits(Rn, dev, dt, shape):
+        _refuse(Rn, "Rn", "of Y's dtype and shape")
+    if dRn is not None:
+        if not _fits(dRn, dev, dt, shape):
+            _refuse(dRn, "dRn", "of Y's dtype and shape")
+        pR = dRn.data_ptr()
+    if dN is not None:
+        if not _fits(dN, dev, dt, shape):
+            _refuse(dN, "dN", "of Y's dtype and shape")
+        pN = dN.data_ptr()
     p = _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, 0.0)
+    if post_weight is not None:
+        p1 = _stat(rstd_post, "rstd_post", dev, M)
+        dw1 = torch.empty_like(post_weight)
+        d1 = dw1.data_ptr()
+    if pre_weight is not None:
+        p2 = _stat(rstd_pre, "rstd_pre", dev, M)
+        dw2 = torch.empty_like(pre_weight)
+        d2 = dw2.data_ptr()
+    if gate is not None:
+        dg = torch.empty_like(gate)
+        dgp = dg.data_ptr()
     dY = torch.empty_like(Y)
     dR = torch.empty_like(Y)
-    dw1 = torch.empty_like(post_weight) if post_weight is not None else None
-    dw2 = torch.empty_like(pre_weight) if pre_weight is not None else None
-    dg = torch.empty_like(gate) if gate is not None else None
+    c = lib()
     ref = ctypes.byref(p)
-    need = lib().swiglu_block_norm_bwd_workspace(ref, M, D, code)
-    ws = None
+    need = c.swiglu_block_norm_bwd_workspace(ref, M, D, code)
+    s = _stream(stream)
     if need > 0:
         # drawn on the current stream; a different stream of the call keeps it
         ws = Y.new_empty((need,), dtype=torch.uint8)
-    s = _stream(stream)
-    if ws is not None and stream is not None and s != torch.cuda.current_stream().cuda_stream:
-        ext = torch.cuda.ExternalStream(s, device=Y.device)
-        ext.wait_stream(torch.cuda.current_stream())  # its memory may still be in use there
-        ws.record_stream(ext)
-
-    def ptr(t):
-        return t.data_ptr() if t is not None else None
-
-    st = lib().swiglu_block_norm_bwd(ptr(dRn), ptr(dN), Y.data_ptr(), Rn.data_ptr(), ptr(rstd_post),
-                                     ptr(rstd_pre), ref, dY.data_ptr(), dR.data_ptr(), ptr(dw1),
-                                     ptr(dw2), ptr(dg), ptr(ws), max(need, 0), M, D, code, s)
+        wsp = ws.data_ptr()
+        if stream is not None and s != torch.cuda.current_stream().cuda_stream:
+            ext = torch.cuda.ExternalStream(s, device=Y.device)
+            ext.wait_stream(torch.cuda.current_stream())  # its memory may still be in use there
+            ws.record_stream(ext)
+    else:
+        need = 0
+    st = c.swiglu_block_norm_bwd(pR, pN, Y.data_ptr(), Rn.data_ptr(), p1, p2, ref, dY.data_ptr(),
+                                 dR.data_ptr(), d1, d2, dgp, wsp, need, M, D, code, s)
     if st:
         _check("swiglu_block_norm_bwd", st)
     return dY, dR, dw1, dw2, dg
