@@ -797,6 +797,7 @@ struct NormReduceArgs {
     void *dw2, *dw1, *dgate;   // null: not wanted here
     int64_t workers;           // blocks of the main kernel
     int splits;                // sums per gate row
+    int64_t gates;             // gate rows
     int D;
     int per_row;               // per-row gates: acc1 holds dW1 itself, accg the gate rows' sums
     float scale;
@@ -805,7 +806,7 @@ struct NormReduceArgs {
 constexpr int kReduceRows = 32;
 
 // Joins the workers' column sums, in a fixed order: blockIdx.y = 0 the
-// weights (and the single gate row), 1 + g gate row g.
+// weights (and the single gate row), the others kReduceRows gate rows each.
 template <bool kBf16>
 __global__ void __launch_bounds__(32 * kReduceRows) block_norm_reduce_kernel(const NormReduceArgs a) {
     __shared__ float part[2][kReduceRows][33];
@@ -819,20 +820,38 @@ __global__ void __launch_bounds__(32 * kReduceRows) block_norm_reduce_kernel(con
         if (kBf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
         else static_cast<float *>(p)[i] = x;
     };
-    const bool gates = blockIdx.y > 0;
-    const int64_t gr = static_cast<int64_t>(blockIdx.y) - 1;
     float v0 = 0.0f, v1 = 0.0f;
     griddep_launch_dependents();
     griddep_wait();
+    // (a batch's loads are in flight together)
+    constexpr int kBatch = 5;
+    if (blockIdx.y > 0) {   // a gate row per row of threads
+        const int64_t gr = static_cast<int64_t>(blockIdx.y - 1) * kReduceRows + ty;
+        if (gr >= a.gates || col >= a.D) return;
+        const float *from = a.accg + gr * a.splits * a.D + col;
+        for (int i0 = 0; i0 < a.splits; i0 += kBatch) {
+            float x[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) x[j] = i0 + j < a.splits ? from[static_cast<int64_t>(i0 + j) * a.D] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) v0 += x[j];
+        }
+        store(a.dgate, gr * a.D + col, a.scale * (a.w1 ? load(a.w1, col) : 1.0f) * v0);
+        return;
+    }
     if (col < a.D) {
-        if (gates) {
-            for (int64_t i = ty; i < a.splits; i += kReduceRows)
-                v0 += a.accg[(gr * a.splits + i) * a.D + col];
-        } else {
-#pragma unroll 5
-            for (int64_t i = ty; i < a.workers; i += kReduceRows) {
-                if (a.acc2) v0 += a.acc2[i * a.D + col];
-                if (a.acc1) v1 += a.acc1[i * a.D + col];
+        for (int64_t i0 = ty; i0 < a.workers; i0 += kReduceRows * kBatch) {
+            float x[kBatch], z[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t i = i0 + j * kReduceRows;
+                x[j] = a.acc2 && i < a.workers ? a.acc2[i * a.D + col] : 0.0f;
+                z[j] = a.acc1 && i < a.workers ? a.acc1[i * a.D + col] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                v0 += x[j];
+                v1 += z[j];
             }
         }
     }
@@ -847,10 +866,6 @@ __global__ void __launch_bounds__(32 * kReduceRows) block_norm_reduce_kernel(con
         v1 += part[1][i][threadIdx.x];
     }
     const float w = a.w1 ? load(a.w1, col) : 1.0f;
-    if (gates) {
-        store(a.dgate, gr * a.D + col, a.scale * w * v0);
-        return;
-    }
     if (a.dw2) store(a.dw2, col, v0);
     if (a.dw1) {
         const float g = a.per_row ? 1.0f : a.scale * (a.gate ? load(a.gate, col) : 1.0f);
@@ -1084,10 +1099,11 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
     r.dgate = n.gate ? dgate : nullptr;
     r.workers = p.blocks;
     r.splits = static_cast<int>(p.splits);
+    r.gates = gates;
     r.D = D;
     r.per_row = per_row ? 1 : 0;
     r.scale = n.scale;
-    const dim3 grid((D + 31) / 32, static_cast<unsigned>(1 + (a.accg ? gates : 0)));
+    const dim3 grid((D + 31) / 32, static_cast<unsigned>(1 + (a.accg ? (gates + kReduceRows - 1) / kReduceRows : 0)));
     const dim3 block(32, kReduceRows);
     return f32 ? launch_dependent(block_norm_reduce_kernel<false>, grid, block, 0, stream, r)
                : launch_dependent(block_norm_reduce_kernel<true>, grid, block, 0, stream, r);
