@@ -54,7 +54,8 @@ static void check(int64_t M, int D, int f32, int64_t gates, int sms) {
     int64_t at = 0;
     for (int64_t item = 0; item < items; ++item) {
         const int64_t gr = item / p.splits, sp = item - gr * p.splits;
-        const int64_t row0 = gr * per + per * sp / p.splits, row1 = gr * per + per * (sp + 1) / p.splits;
+        const int64_t each = per / p.splits, longer = per % p.splits;
+        const int64_t row0 = gr * per + sp * each + std::min(sp, longer), row1 = row0 + each + (sp < longer ? 1 : 0);
         REQUIRE(row0 == at && row1 > row0 && row1 <= (gr + 1) * per);
         at = row1;
     }

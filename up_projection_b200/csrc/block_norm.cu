@@ -291,7 +291,8 @@ __device__ __noinline__ void ring_abandon(uint32_t full, int stages, int stage, 
 // copy bandwidth (the two barriers of a row leave the rest).
 template <bool kBf16, int kV>
 __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const NormArgs a, const int T, const int groups,
-                                                                          const int stages) {
+                                                                          const int stages, const int64_t rows,
+                                                                          const int longer) {
     using E = Vec<kBf16>;
     constexpr int kE = E::kE, kP = kE / 2;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -318,7 +319,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_ring_kernel(const 
     __syncthreads();
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t row0 = a.M * blockIdx.x / gridDim.x + grp, row1 = a.M * (blockIdx.x + 1) / gridDim.x;
+    const int b = blockIdx.x;   // `rows` rows each, the first `longer` blocks one more
+    const int64_t row0 = b * rows + min(b, longer) + grp, row1 = (b + 1) * rows + min(b + 1, longer);
     auto copy_row = [&](int64_t row, int to) {
         const uint32_t fb = full + 8 * to, st = ring + to * 2u * pitch;
         mbar_arrive_expect_tx(fb, 2u * row_bytes);
@@ -438,7 +440,9 @@ struct NormBwdArgs {
     float *acc2, *acc1, *accg;       // workspaces: [blocks][D], [blocks][D], [items][D]
     int64_t rows_per_gate;           // rows of one gate row (all of them without per-row gates)
     int64_t gates;                   // gate rows (1 without)
-    int splits;                      // blocks that share a gate row's rows
+    int splits;                      // blocks that share a gate row's rows:
+    int64_t rows_per_item;           // so many each,
+    int longer;                      // and the first ones one more
     int D;
     int T, groups;                   // threads per row, rows at a time
     int stages;                      // rows of a group's ring
@@ -488,10 +492,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_bwd_kernel(const N
     __syncthreads();
     griddep_wait();
     const int64_t items = a.gates * a.splits;
+    // (items fit 32 bits; the first copy waits for this)
+    auto gate_of = [&](int64_t item) -> int64_t {
+        return kGates ? static_cast<uint32_t>(item) / static_cast<uint32_t>(a.splits) : 0u;
+    };
     auto rows_of = [&](int64_t item, int64_t &row0, int64_t &row1) {
-        const int64_t gr = item / a.splits, sp = item - gr * a.splits;
-        row0 = gr * a.rows_per_gate + a.rows_per_gate * sp / a.splits;
-        row1 = gr * a.rows_per_gate + a.rows_per_gate * (sp + 1) / a.splits;
+        const int64_t gr = gate_of(item), sp = item - gr * a.splits;
+        row0 = gr * a.rows_per_gate + sp * a.rows_per_item + (sp < a.longer ? sp : a.longer);
+        row1 = row0 + a.rows_per_item + (sp < a.longer ? 1 : 0);
     };
 
     auto copy_row = [&](int64_t row, int to) {
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) block_norm_bwd_kernel(const N
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         int64_t row0, row1;
         rows_of(item, row0, row1);
-        const int64_t gr = item / a.splits;
+        const int64_t gr = gate_of(item);
         const uint4 *gate = a.gate ? a.gate + gr * nvec : nullptr;
         if constexpr (kHold) {
 #pragma unroll
@@ -966,7 +974,7 @@ cudaError_t launch_fwd_ring(const NormArgs &a, const RingShape &s, const DeviceI
     int stages = static_cast<int>(kRingRoom / (row * s.groups));
     if (stages > kMaxRing) stages = kMaxRing;
     return launch_dependent(kernel, dev.sm_count, s.T * s.groups, stages * row * s.groups, stream, a, s.T, s.groups,
-                            stages);
+                            stages, a.M / dev.sm_count, static_cast<int>(a.M % dev.sm_count));
 }
 
 template <bool kBf16, int kV>
@@ -1081,6 +1089,8 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
     a.rows_per_gate = per_row ? M / gates : M;
     a.gates = gates;
     a.splits = static_cast<int>(p.splits);
+    a.rows_per_item = a.rows_per_gate / p.splits;
+    a.longer = static_cast<int>(a.rows_per_gate % p.splits);
     a.D = D;
     a.T = p.T;
     a.groups = p.groups;
