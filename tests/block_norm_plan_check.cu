@@ -26,15 +26,17 @@ static int checked = 0;
 
 static void check(int64_t M, int D, int f32, int64_t gates, int sms) {
     const int nvec = D / (f32 ? 4 : 8);
-    const RingShape s = ring_shape(D, f32);
+    const RingShape s = ring_shape(D, f32, true), fs = ring_shape(D, f32, false);
     REQUIRE(s.T % 32 == 0 && s.T * s.v >= nvec && s.T <= kRingThreads);
     REQUIRE(s.groups >= 1 && s.groups <= kMaxGroups && s.groups * s.T <= kRingThreads);
     REQUIRE(s.T == 32 || s.groups <= 8);   // slots and named barriers
     REQUIRE(f32 ? (s.v == 2 || s.v == 4) : (s.v == 1 || s.v == 2 || s.v == 4));
-    if (nvec >= 512 && s.v * (f32 ? 4 : 8) <= 16) {   // the forward's ring
-        REQUIRE(s.v == (f32 ? 4 : 2));
-        const uint32_t row = 2u * 16u * s.v * s.T;
-        REQUIRE(kRingRoom / (row * s.groups) >= 2);
+    if (nvec >= 64 && fs.v * (f32 ? 4 : 8) <= 16) {   // the forward's ring
+        REQUIRE(fs.v == (f32 ? 4 : 2) && fs.T % 32 == 0 && fs.T * fs.v >= nvec && fs.T <= kRingThreads);
+        REQUIRE(fs.groups >= 1 && fs.groups <= kMaxGroups && fs.groups * fs.T <= kRingThreads);
+        REQUIRE(fs.T == 32 || fs.groups <= 8);
+        const uint32_t row = 2u * 16u * fs.v * fs.T;
+        REQUIRE(kRingRoom / (row * fs.groups) >= 2);
     }
     const bool per_row = gates > 1;
     const BwdPlan p = bwd_plan(M, D, f32, per_row, gates, true, true, true, sms);

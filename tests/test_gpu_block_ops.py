@@ -768,3 +768,12 @@ def test_gemm_row_counts_are_exact(M, N, K, block):
 @pytest.mark.parametrize("M,K", [(33, 2192), (60, 2176), (64, 2192), (65, 2192), (128, 384)])
 def test_gated_row_counts_are_exact(M, K, order):
     test_gated_weights_in_any_place(M, K, order)
+
+
+@pytest.mark.parametrize("dtype,M,D", [("bf16", 4800, 512), ("bf16", 2400, 1032), ("bf16", 1200, 2048),
+                                       ("bf16", 5000, 520), ("f32", 4800, 256), ("f32", 2500, 500),
+                                       ("f32", 1300, 1024), ("bf16", 620, 4104)])
+@pytest.mark.parametrize("post,pre,gate", [(True, True, "groups"), (False, True, "channel"),
+                                           (True, False, "none"), (False, False, "rows")])
+def test_norm_shorter_rows_through_rings(dtype, M, D, post, pre, gate):
+    test_norm_many_rows_matches_fp64(dtype, M, D, post, pre, gate)

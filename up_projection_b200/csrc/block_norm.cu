@@ -897,16 +897,17 @@ RowShape row_shape(int nvec) {
     return s;
 }
 
-// Ring kernels: 16 elements per thread (8 for short rows, 32 for bf16 rows of
-// more than 8192), whole warps per row, row groups up to kRingThreads.
+// Ring kernels: 16 elements per thread (backward: 8 for rows of up to 1024,
+// M = 2368, D = 1024 12.1 against 12.8 us; 32 for bf16 rows of more than 8192),
+// whole warps per row, row groups up to kRingThreads.
 struct RingShape {
     int v, T, groups;
 };
 
-RingShape ring_shape(int D, int f32) {
+RingShape ring_shape(int D, int f32, bool backward) {
     RingShape s{};
     const int nvec = D / (f32 ? 4 : 8), two = f32 ? 4 : 2;   // vectors of 16 elements
-    s.v = nvec <= 64 * two ? two / 2 : (nvec <= 512 * two ? two : 4);
+    s.v = backward && nvec <= 64 * two ? two / 2 : (nvec <= 512 * two ? two : 4);
     s.T = (((nvec + s.v - 1) / s.v) + 31) / 32 * 32;
     s.groups = kRingThreads / s.T;
     if (s.groups > kMaxGroups) s.groups = kMaxGroups;   // (T = 32; with more threads it is 8 or fewer)
@@ -938,7 +939,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(int64_t M, int D, int f32, bool per_row, int64_t gates, bool w1, bool w2, bool gate,
                  int sm_count) {
     BwdPlan p{};
-    const RingShape sh = ring_shape(D, f32);
+    const RingShape sh = ring_shape(D, f32, true);
     p.v = sh.v;
     p.T = sh.T;
     p.groups = sh.groups;
@@ -988,14 +989,17 @@ cudaError_t launch_fwd_v(const NormArgs &a, const RowShape &s, int sm_count, cud
 
 template <bool kBf16>
 cudaError_t launch_fwd(const NormArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
-    const RingShape r = ring_shape(a.D, !kBf16);
+    const RingShape r = ring_shape(a.D, !kBf16, false);
     const int nvec = a.D / Vec<kBf16>::kE;
-    // Rings for rows of 8 KB up to what holds its weights in registers, from
-    // four rows per row group on.  Ring against plain, B200: M = 8192,
-    // D = 4096 bf16 50.0 against 52.8 us; M = 777, D = 5120 fp32 12.7 against
-    // 17.0; outside, M = 512, D = 4096 6.3 against 4.9; M = 4096, D = 1024
-    // 11.9 against 9.9; M = 2048, D = 16384 75 against 67.
-    if (nvec >= 512 && r.v * Vec<kBf16>::kE <= 16 && a.M >= 4 * static_cast<int64_t>(dev.sm_count) * r.groups)
+    // Rings for rows of 1 KB up to what holds its weights in registers, from
+    // two rows per row group on (four where two or fewer groups share a block).
+    // Ring against plain, B200, us: 8192 x 4096 bf16 48.2 against 52.8, 16384 x
+    // 2048 49.0 and 70.1, 16384 x 512 15.7 and 17.9, 777 x 5120 fp32 11.6 and
+    // 17.0; at the limits 4736 x 512 5.1 and 5.6, 2368 x 1024 5.7 and 5.8, 1184 x
+    // 4096 9.1 and 9.1; outside, 592 x 4096 5.6 and 4.6, 18944 x 256 10.9 and
+    // 9.6, 2048 x 16384 75 and 67.
+    if (nvec >= 64 && r.v * Vec<kBf16>::kE <= 16 &&
+        a.M >= (r.groups >= 4 ? 2 : 4) * static_cast<int64_t>(dev.sm_count) * r.groups)
         return launch_fwd_ring<kBf16, kBf16 ? 2 : 4>(a, r, dev, stream);
     const RowShape s = row_shape(nvec);
     switch (s.v) {
