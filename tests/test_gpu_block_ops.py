@@ -777,3 +777,57 @@ def test_gated_row_counts_are_exact(M, K, order):
                                            (True, False, "none"), (False, False, "rows")])
 def test_norm_shorter_rows_through_rings(dtype, M, D, post, pre, gate):
     test_norm_many_rows_matches_fp64(dtype, M, D, post, pre, gate)
+
+
+def test_native_and_ctypes_calls_agree(monkeypatch):
+    """The native binding and the path through ctypes: the same outputs, layouts
+    and refusals."""
+    from up_projection_b200 import _capi
+    v = norm_inputs(12, 256, "bf16", True, True, 3)
+    for t in v.values():
+        t.requires_grad_(True)
+    x = rand((37, 400), 1, torch.bfloat16)
+
+    def calls():
+        Rn, N, r1, r2 = up.swiglu_block_norm(v["Y"], v["R"], v["post"], v["pre"], v["gate"], return_stats=True)
+        out = [Rn, N, r1, r2, *up.swiglu_block_norm(v["Y"], v["R"])[:1],
+               *up.swiglu_block_norm_bwd(Rn, N, v["Y"], Rn, r1, r2, v["post"], v["pre"], v["gate"]),
+               *[t for t in up.swiglu_block_norm_bwd(Rn, None, v["Y"], Rn, None, None) if t is not None]]
+        for block in ("row", "tile"):
+            for transpose in (False, True):
+                out += up.swiglu_quant_b128(x, block, transpose)
+        q, s = up.swiglu_quant_b128(x.view(1, 37, 400))
+        w, ws = up.swiglu_quant_b128(rand((264, 400), 2, torch.bfloat16), "tile")
+        out += [q, s, up.swiglu_gemm_b128(q, s, w, ws), up.swiglu_gemm_b128(q, s, w, ws, out_dtype=torch.float32)]
+        out += up.swiglu_fwd_b128(q, s, w, ws, w, ws, return_gu=True)
+        out.append(up.swiglu_fwd_b128(q[0].view(torch.float8_e4m3fn), s, w, ws, w, ws, activation=up.SWIGLU_ACT_GELU_TANH,
+                                      gate_multiplier=2))
+        H = torch.empty((37, 264), dtype=torch.bfloat16, device=dev())
+        assert up.swiglu_gemm_b128(q, s, w, ws, Y=H) is H and up.swiglu_fwd_b128(q, s, w, ws, w, ws, H=H) is H
+        with pytest.raises(up.SwigluError):
+            up.swiglu_block_norm(v["Y"], v["R"], v["post"], v["pre"], v["post"].expand(5, 256).contiguous())
+        with pytest.raises(up.SwigluError):
+            up.swiglu_block_norm(v["Y"], v["R"], residual_scale=float("inf"))
+        with pytest.raises(up.SwigluError):
+            up.swiglu_quant_b128(x[:, :392].contiguous())
+        with pytest.raises(up.SwigluError):
+            up.swiglu_gemm_b128(q, s, w[:9].contiguous(), ws[:1].contiguous())
+        with pytest.raises(up.SwigluError):
+            up.swiglu_fwd_b128(q, s, w, ws, w, ws, activation=9)
+        for bad in ((v["Y"], v["R"][:6]), (v["Y"], v["R"].float()), (v["Y"].t(), v["R"]), (v["Y"].cpu(), v["R"])):
+            with pytest.raises((ValueError, TypeError)):
+                up.swiglu_block_norm(*bad)
+        with pytest.raises(ValueError):
+            up.swiglu_gemm_b128(q, s[:36], w, ws)
+        synced()
+        return out
+
+    native = _capi._native
+    assert native is not None
+    a = calls()
+    monkeypatch.setattr(_capi, "_native", None)
+    b = calls()
+    assert len(a) == len(b)
+    for s, t in zip(a, b):
+        assert s.dtype == t.dtype and s.shape == t.shape and s.stride() == t.stride() and torch.equal(s, t)
+        assert not s.requires_grad and not t.requires_grad

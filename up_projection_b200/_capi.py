@@ -131,7 +131,26 @@ def lib() -> ctypes.CDLL:
                 f.restype = res
                 f.argtypes = args
             _lib = handle
+            _bind(handle)
     return _lib
+
+
+# csrc/binding.cpp: the calls of the operators around the projection that are in
+# order, done natively (None: not built for this torch, or not loaded yet).  A
+# native call returns None for what it leaves to the functions below.
+_native = None
+
+
+def _bind(handle):
+    global _native
+    try:
+        from . import _binding
+    except ImportError:
+        return
+    _binding.bind(*(ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in (
+        "swiglu_block_norm", "swiglu_block_norm_bwd_workspace", "swiglu_block_norm_bwd",
+        "swiglu_quant_b128", "swiglu_gemm_b128", "swiglu_fwd_b128")))
+    _native = _binding
 
 
 def status_string(status: int) -> str:
@@ -415,6 +434,12 @@ def swiglu_quant_b128(X: torch.Tensor, block: str = "row", transpose: bool = Fal
     tile = block == "tile"
     if not tile and block != "row":
         raise ValueError('block must be "row" or "tile"')
+    if stream is None and _native is not None:
+        r = _native.quant_b128(X, tile, transpose)
+        if r is not None:
+            if type(r) is int:
+                _check("swiglu_quant_b128", r)
+            return r
     if not (X.is_cuda and X.is_contiguous()):
         _dev(X, "X")
     code = _DT.get(X.dtype)
@@ -448,6 +473,12 @@ def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: tor
     Bs [ceil(N/128), KB] (128 x 128 blocks) or [N, KB] (1 x 128, rows innermost
     in memory); KB = ceil(K/128), K a multiple of 16, N of 8.  Y bf16 or fp32
     with A's leading dims."""
+    if stream is None and _native is not None and (out_dtype is torch.bfloat16 or out_dtype is torch.float32):
+        r = _native.gemm_b128(A, As, B, Bs, out_dtype is torch.float32, Y)
+        if r is not None:
+            if type(r) is int:
+                _check("swiglu_gemm_b128", r)
+            return r
     dev = _device_of(A, "A")
     _codes(A, "A", dev)
     _codes(B, "B", dev)
@@ -491,6 +522,12 @@ def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: to
     """swiglu_fwd on block-scaled e4m3 operands: X [..., K] codes with 1 x 128
     scales Xs [M, KB], Wg, Wu [N, K] codes with 128 x 128 scales
     [ceil(N/128), KB].  Returns H bf16 [..., N], or (H, G, U)."""
+    if stream is None and _native is not None:
+        r = _native.fwd_b128(X, Xs, Wg, Wgs, Wu, Wus, H, activation, gate_multiplier, return_gu)
+        if r is not None:
+            if type(r) is int:
+                _check("swiglu_fwd_b128", r)
+            return r
     dev = _device_of(X, "X")
     _codes(X, "X", dev)
     _codes(Wg, "Wg", dev)
@@ -586,6 +623,12 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
     m // (M / rows)).  Returns (Rn, N), with return_stats=True (training)
     (Rn, N, rstd_post, rstd_pre), fp32 [M], for swiglu_block_norm_bwd.  Rn may
     be given as the output buffer, R itself included (in place)."""
+    if stream is None and _native is not None:
+        r = _native.block_norm(Y, R, post_weight, pre_weight, gate, residual_scale, eps, return_stats, Rn)
+        if r is not None:
+            if type(r) is int:
+                _check("swiglu_block_norm", r)
+            return r
     dev, dt, code, shape, M, D = _norm_shape(Y)
     if not _fits(R, dev, dt, shape):
         _refuse(R, "R", "of Y's dtype and shape")
@@ -629,6 +672,13 @@ def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: 
     d_pre, d_gate), the last three None without their parameter (d_gate has
     gate's shape).  dRn or dN may be None for zero (dN only without
     pre_weight); Rn, rstd_post, rstd_pre as the forward returned them."""
+    if stream is None and _native is not None:
+        r = _native.block_norm_bwd(dRn, dN, Y, Rn, rstd_post, rstd_pre, post_weight, pre_weight, gate,
+                                   residual_scale)
+        if r is not None:
+            if type(r) is int:
+                _check("swiglu_block_norm_bwd", r)
+            return r
     dev, dt, code, shape, M, D = _norm_shape(Y)
     if (dN is None) != (pre_weight is None):
         raise ValueError("dN and pre_weight go together")

@@ -6,7 +6,9 @@ Each ``csrc/*.cu`` is compiled to an object under ``_build/`` (in parallel),
 then linked into ``up_projection_b200/libswiglu_b200.so`` with the CUDA
 runtime linked statically, so the library needs only the driver at run time.
 ``-Xptxas -v`` output (registers, spills, shared memory per kernel) is kept
-in ``_build/ptxas.log``.
+in ``_build/ptxas.log``.  ``csrc/binding.cpp``, the native calls of the
+operators around the projection, becomes ``_binding.so`` next to it (g++, torch's
+headers); without it those calls go through ctypes.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libswiglu_b200.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -52,6 +55,34 @@ def up_to_date() -> bool:
     return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
 
 
+def binding_up_to_date() -> bool:
+    deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "swiglu.h"), os.path.abspath(__file__)]
+    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in deps)
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp against this interpreter and its torch."""
+    if not force and binding_up_to_date():
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", "-I" + sysconfig.get_paths()["include"], f"-I{base}/include",
+           f"-I{base}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{base}/lib", "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError("binding failed:\n" + p.stdout + p.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _compile(src: str):
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
     cmd = [nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj]
@@ -60,6 +91,7 @@ def _compile(src: str):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
