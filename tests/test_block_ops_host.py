@@ -181,3 +181,22 @@ def test_no_device_is_an_error():
     assert lib.swiglu_fwd_b128(*A[:7], 4, 64, 64, None, None) == none
     assert lib.swiglu_block_norm(A[0], A[1], _p(A[8], A[9]), A[2], A[3], None, None, 4, 64, 0,
                                  None) == none
+
+
+def test_native_binding_leaves_other_calls_alone():
+    """The native calls return None for what is not a call in order: CPU
+    tensors, other objects, other numbers of arguments."""
+    _capi.lib()
+    b = _capi._native
+    assert b is not None
+    x, s = torch.zeros(4, 64), torch.zeros(4, 1)
+    q = torch.zeros(4, 64, dtype=torch.uint8)
+    assert b.quant_b128(x, False, False) is None and b.quant_b128(x) is None and b.quant_b128([1.0], True, True) is None
+    assert b.block_norm(x, x, None, None, None, 1.0, 1e-6, False, None) is None
+    assert b.block_norm(None, None, None, None, None, 1.0, 1e-6, False, None) is None
+    assert b.block_norm(x, x, None, None, None, "1", None, False, None) is None
+    assert b.block_norm_bwd(x, None, x, x, None, None, None, None, None, 1.0) is None
+    assert b.gemm_b128(q, s, q, s, False, None) is None and b.gemm_b128(None, s, q, s, True, 3) is None
+    assert b.fwd_b128(q, s, q, s, q, s, None, 0, 1.0, False) is None
+    with pytest.raises((TypeError, ValueError)):
+        b.bind(0, 0, 0, 0, 0, 0)
