@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  const __grid_constant__ CUtensorMap tm_y,
                                  const __grid_constant__ CUtensorMap tm_yg,
                                  const __grid_constant__ CUtensorMap tm_yu,
-                                 const float *__restrict__ bs0, const float *__restrict__ bs1,
+                                 const float *bs0, const float *bs1,
                                  const Out out, int M, int N, const PairPlan p) {
     using L = PairLayout<kMode>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int kb = 0; kb < num_kb; kb += kSlotBlocks) {
                     float v = 0.0f;
-                    if (kMode != kRowScales) v = __ldg(src + min(kb + lane / 8, num_kb - 1));
+                    if (kMode != kRowScales) v = ld_plain(src + min(kb + lane / 8, num_kb - 1));
                     if (!mbar_wait_long(bar_sempty + 8 * slot, phase ^ 1u, abort_flag)) {
                         failed = true;
                         break;

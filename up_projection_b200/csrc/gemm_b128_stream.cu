@@ -88,7 +88,7 @@ struct StreamMaps {
 template <int kMode, int kTok>
 __global__ void __launch_bounds__(kThreads, 1)
     swiglu_gemm_b128_stream_kernel(const __grid_constant__ StreamMaps maps,
-                                   const float *__restrict__ bs0, const float *__restrict__ bs1,
+                                   const float *bs0, const float *bs1,
                                    const Out out, int M, int N, int num_kb, int joined, int swapped,
                                    const StreamPlan p) {
     constexpr int kRt = 2;   // groups of 128 rows a warp can hold
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = kb_begin; kb < kb_end && !failed; kb += nb) {
                     step_of(kb, nb);
                     float v = 0.0f;
-                    if (kMode != kRowScales && lane < 4 * p.kbs) v = __ldg(src + min(kb + lane / 4, num_kb - 1));
+                    if (kMode != kRowScales && lane < 4 * p.kbs) v = ld_plain(src + min(kb + lane / 4, num_kb - 1));
                     if (!mbar_wait_long(bar_sempty + 8 * slot, sphase ^ 1u, abort_flag)) {
                         failed = true;
                         break;
