@@ -1,0 +1,68 @@
+"""Contracts of the operators around the projection on a B200 that the tests of
+their results do not reach."""
+import pytest
+import torch
+
+import up_projection_b200 as up
+from gpu_util import dev
+from test_gpu_block_ops import rand
+
+pytestmark = pytest.mark.gpu
+
+
+def _stream_calls():
+    """name -> (call on a stream, bytes of its first output)."""
+    M, D, N = 512, 1024, 520
+    bf = torch.bfloat16
+    x, w = rand((M, D), 1, bf), rand((D,), 2, bf)
+    (a, sa), (b, sb) = up.swiglu_quant_b128(x), up.swiglu_quant_b128(rand((N, D), 3, bf), "tile")
+    Rn, _, r1, r2 = up.swiglu_block_norm(x, x, w, w, return_stats=True)
+    return {
+        "quant": (lambda s: up.swiglu_quant_b128(x, stream=s), M * D),
+        "gemm": (lambda s: (up.swiglu_gemm_b128(a, sa, b, sb, stream=s),), 2 * M * N),
+        "gated": (lambda s: up.swiglu_fwd_b128(a, sa, b, sb, b, sb, return_gu=True, stream=s), 2 * M * N),
+        "norm": (lambda s: up.swiglu_block_norm(x, x, w, w, return_stats=True, stream=s), 2 * M * D),
+        "norm_bwd": (lambda s: up.swiglu_block_norm_bwd(x, x, x, Rn, r1, r2, w, w, stream=s), 2 * M * D),
+    }
+
+
+@pytest.mark.parametrize("name", ["quant", "gemm", "gated", "norm", "norm_bwd"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_drawn_for_another_stream_wait_for_their_memory(name, handle):
+    """Outputs are drawn on the current stream: their memory may be that of
+    tensors whose last reader there has not run yet."""
+    call, nbytes = _stream_calls()[name]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in call(None) if t is not None]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.full((nbytes,), 85, dtype=torch.uint8, device=dev()) for _ in range(6)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)            # some 10 ms
+        copies = [t.clone() for t in old]
+        del old                                  # back to the allocator, still to be read
+        got = call(side.cuda_stream if handle else side)
+        torch.cuda.synchronize()
+        assert all(bool((c == 85).all()) for c in copies)
+        for g, t in zip(got, want):
+            assert torch.equal(g, t)
+
+
+def test_call_on_a_stream_that_captures_beside_the_current_one():
+    """The current stream does not capture, the call's does: no wait between
+    them, which would end the capture."""
+    x = rand((64, 256), 1, torch.bfloat16)
+    want = up.swiglu_quant_b128(x)
+    side = torch.cuda.Stream()
+    up.swiglu_quant_b128(x, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        g.capture_begin(capture_error_mode="relaxed")
+    got = up.swiglu_quant_b128(x, stream=side)
+    with torch.cuda.stream(side):
+        g.capture_end()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

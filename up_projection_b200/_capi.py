@@ -173,6 +173,28 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _drawn(stream, *tensors) -> int:
+    """The call's stream as a handle, after outputs and scratch were drawn on
+    the current one.  Another stream first waits for what may still use their
+    memory there, and keeps it until its own work is done.  (A stream that
+    captures cannot wait for one that does not.)"""
+    s = _stream(stream)
+    if stream is None:
+        return s
+    current = torch.cuda.current_stream()
+    if s != current.cuda_stream:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            captures = torch.cuda.is_current_stream_capturing()
+        if not captures or torch.cuda.is_current_stream_capturing():
+            stream.wait_stream(current)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return s
+
+
 def _check(fn: str, st: int):
     if st != SWIGLU_OK:
         raise SwigluError(fn, st)
@@ -459,7 +481,7 @@ def swiglu_quant_b128(X: torch.Tensor, block: str = "row", transpose: bool = Fal
     else:
         S = X.new_empty_strided((rows, kb), (1, rows), dtype=torch.float32)
     st = lib().swiglu_quant_b128(X.data_ptr(), Q.data_ptr(), S.data_ptr(), R, C, code,
-                                 1 if tile else 0, 1 if transpose else 0, _stream(stream))
+                                 1 if tile else 0, 1 if transpose else 0, _drawn(stream, Q, S))
     if st:
         _check("swiglu_quant_b128", st)
     return Q, S
@@ -501,15 +523,16 @@ def swiglu_gemm_b128(A: torch.Tensor, As: torch.Tensor, B: torch.Tensor, Bs: tor
     code = _DT.get(out_dtype)
     if code is None:
         raise TypeError(f"unsupported out_dtype {out_dtype}; use bfloat16 or float32")
+    drawn = None
     if Y is None:
-        Y = A.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
+        Y = drawn = A.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=out_dtype)
     else:
         _dev(Y, "Y")
         _here(Y)
         if Y.dtype != out_dtype or Y.numel() != M * N:
             raise ValueError("Y has the wrong dtype or size")
     st = lib().swiglu_gemm_b128(A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(),
-                                Y.data_ptr(), M, N, K, block, code, _stream(stream))
+                                Y.data_ptr(), M, N, K, block, code, _drawn(stream, drawn))
     if st:
         _check("swiglu_gemm_b128", st)
     return Y
@@ -546,8 +569,9 @@ def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: to
         _refuse(Wgs, "Wgs", f"float32 [{tiles[0]}, {kb}]")
     if not _fits(Wus, dev, torch.float32, tiles):
         _refuse(Wus, "Wus", f"float32 [{tiles[0]}, {kb}]")
+    drawn = None
     if H is None:
-        H = X.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=torch.bfloat16)
+        H = drawn = X.new_empty((M, N) if len(shape) == 2 else (*shape[:-1], N), dtype=torch.bfloat16)
     else:
         _dev(H, "H")
         _here(H)
@@ -561,7 +585,8 @@ def swiglu_fwd_b128(X: torch.Tensor, Xs: torch.Tensor, Wg: torch.Tensor, Wgs: to
         epi = ctypes.byref(Epilogue(int(activation), float(gate_multiplier),
                                     G.data_ptr() if return_gu else None, U.data_ptr() if return_gu else None))
     st = lib().swiglu_fwd_b128(X.data_ptr(), Xs.data_ptr(), Wg.data_ptr(), Wgs.data_ptr(),
-                               Wu.data_ptr(), Wus.data_ptr(), H.data_ptr(), M, K, N, epi, _stream(stream))
+                               Wu.data_ptr(), Wus.data_ptr(), H.data_ptr(), M, K, N, epi,
+                               _drawn(stream, drawn, G, U))
     if st:
         _check("swiglu_fwd_b128", st)
     return (H, G, U) if return_gu else H
@@ -633,8 +658,9 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
     if not _fits(R, dev, dt, shape):
         _refuse(R, "R", "of Y's dtype and shape")
     p = _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, eps)
+    drawn = None
     if Rn is None:
-        Rn = torch.empty_like(R)
+        Rn = drawn = torch.empty_like(R)
     elif not _fits(Rn, dev, dt, shape):
         _refuse(Rn, "Rn", "of Y's dtype and shape")
     N = torch.empty_like(Y) if pre_weight is not None else None
@@ -648,7 +674,7 @@ def swiglu_block_norm(Y: torch.Tensor, R: torch.Tensor, post_weight: torch.Tenso
                                  N.data_ptr() if N is not None else None,
                                  r1.data_ptr() if r1 is not None else None,
                                  r2.data_ptr() if r2 is not None else None, M, D, code,
-                                 _stream(stream))
+                                 _drawn(stream, drawn, N, r1, r2))
     if st:
         _check("swiglu_block_norm", st)
     return (Rn, N, r1, r2) if return_stats else (Rn, N)
@@ -710,19 +736,14 @@ def swiglu_block_norm_bwd(dRn: torch.Tensor | None, dN: torch.Tensor | None, Y: 
     c = lib()
     ref = ctypes.byref(p)
     need = c.swiglu_block_norm_bwd_workspace(ref, M, D, code)
-    s = _stream(stream)
     if need > 0:
-        # drawn on the current stream; a different stream of the call keeps it
         ws = Y.new_empty((need,), dtype=torch.uint8)
         wsp = ws.data_ptr()
-        if stream is not None and s != torch.cuda.current_stream().cuda_stream:
-            ext = torch.cuda.ExternalStream(s, device=Y.device)
-            ext.wait_stream(torch.cuda.current_stream())  # its memory may still be in use there
-            ws.record_stream(ext)
     else:
         need = 0
     st = c.swiglu_block_norm_bwd(pR, pN, Y.data_ptr(), Rn.data_ptr(), p1, p2, ref, dY.data_ptr(),
-                                 dR.data_ptr(), d1, d2, dgp, wsp, need, M, D, code, s)
+                                 dR.data_ptr(), d1, d2, dgp, wsp, need, M, D, code,
+                                 _drawn(stream, dY, dR, dw1, dw2, dg, ws))
     if st:
         _check("swiglu_block_norm_bwd", st)
     return dY, dR, dw1, dw2, dg
