@@ -3,6 +3,7 @@ their results do not reach."""
 import pytest
 import torch
 
+import block_ref as ref
 import up_projection_b200 as up
 from gpu_util import dev
 from test_gpu_block_ops import rand
@@ -66,3 +67,22 @@ def test_call_on_a_stream_that_captures_beside_the_current_one():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("R,C", [(1, 16), (5, 144), (121, 272), (130, 400), (250, 128), (268, 272)])
+def test_transposed_codes_behind_the_rows_are_zero(R, C, block, dtype):
+    """Columns R.. of a transposed Q are 0, also in a block that holds NaN or
+    Inf (whose own codes are 0x7F)."""
+    x = rand((R, C), R + C, torch.float32)
+    x[R - 1, 0] = float("nan")
+    x[0, C // 2] = float("inf")
+    x[R // 2, C - 1] = float("-inf")
+    x = x.to(dtype)
+    q, s = up.swiglu_quant_b128(x, block=block, transpose=True)
+    wq, ws = ref.quant(x, block, True)
+    wq[:, R:] = 0
+    assert q.shape == (C, (R + 15) // 16 * 16)
+    assert torch.equal(q, wq)
+    assert torch.equal(torch.nan_to_num(s.double(), nan=-1.0), torch.nan_to_num(ws, nan=-1.0))
