@@ -1,7 +1,12 @@
 """Contracts of the operators around the projection that hold by construction
 or on the host, without a GPU."""
+import ctypes
 import os
 import re
+
+import pytest
+
+from up_projection_b200 import _capi
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "up_projection_b200", "csrc")
 
@@ -22,3 +27,29 @@ def test_early_started_kernels_read_with_plain_loads():
     for n in early + ["b128.cuh", "pdl.cuh"]:
         found = re.findall(r"__ldg|ld_nc\w*|\.nc\b|__restrict__", _code(os.path.join(CSRC, n)))
         assert not found, (n, found)
+
+
+def _params(post=None, pre=None, gate=None, rows=1):
+    return ctypes.byref(_capi.BlockNormParams(post, pre, gate, rows, 1.0, 1e-6))
+
+
+@pytest.mark.parametrize("D", [1 << 60, 1 << 61, 1 << 62, (1 << 63) - 16, (1 << 62) + 64])
+@pytest.mark.parametrize("dtype", [_capi.SWIGLU_BF16, _capi.SWIGLU_FP32])
+def test_norm_row_lengths_whose_bytes_wrap_are_refused(D, dtype):
+    """D times the element size wraps 64 bits to something small."""
+    lib, a = _capi.lib(), [(i + 1) << 24 for i in range(16)]
+    dim = _capi.SWIGLU_ERR_BAD_DIM
+    assert lib.swiglu_block_norm(a[0], a[1], _params(a[2], a[3]), a[4], a[5], None, None, 4, D, dtype, None) == dim
+    assert lib.swiglu_block_norm_bwd(*a[:6], _params(a[6], a[7]), *a[8:12], None, a[12], 1 << 22, 4, D, dtype,
+                                     None) == dim
+    assert lib.swiglu_block_norm_bwd_workspace(_params(a[6], a[7]), 4, D, dtype) == -1
+
+
+@pytest.mark.parametrize("rows", [1 << 31, 1 << 55, (1 << 63) - 1])
+def test_gate_rows_whose_bytes_wrap_are_refused(rows):
+    """No rows: any number of gate rows divides them, up to the largest M."""
+    lib, a = _capi.lib(), [(i + 1) << 24 for i in range(16)]
+    dim = _capi.SWIGLU_ERR_BAD_DIM
+    p = _params(gate=a[6], rows=rows)
+    assert lib.swiglu_block_norm(a[0], a[1], p, a[4], None, None, None, 0, 64, 0, None) == dim
+    assert lib.swiglu_block_norm_bwd(*a[:6], p, a[8], a[9], None, None, a[10], None, 0, 0, 64, 0, None) == dim

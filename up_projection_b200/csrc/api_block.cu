@@ -47,11 +47,11 @@ int check_spans(const Span *in, int n_in, const Span *out, int n_out, const int 
 int check_norm_shape(int64_t M, int64_t D, int dtype, const swiglu_block_norm_params *p) {
     if (!p) return SWIGLU_ERR_NULL_POINTER;
     if (dtype != SWIGLU_BF16 && dtype != SWIGLU_FP32) return SWIGLU_ERR_BAD_DTYPE;
-    if (M < 0 || D < 0 || M > kMaxDim || D * elem_size(dtype) > kNormRowBytes) return SWIGLU_ERR_BAD_DIM;
+    if (M < 0 || D < 0 || M > kMaxDim || D > kNormRowBytes / elem_size(dtype)) return SWIGLU_ERR_BAD_DIM;
     if (D * elem_size(dtype) % 16 != 0) return SWIGLU_ERR_MISALIGNED_DIM;
     if (!isfinite(p->residual_scale) || !isfinite(p->eps) || p->eps < 0.0f)
         return SWIGLU_ERR_BAD_EPILOGUE;
-    if (p->gate && (p->gate_rows < 1 || (M > 0 && (p->gate_rows > M || M % p->gate_rows != 0))))
+    if (p->gate && (p->gate_rows < 1 || p->gate_rows > kMaxDim || (M > 0 && M % p->gate_rows != 0)))
         return SWIGLU_ERR_BAD_DIM;
     return SWIGLU_OK;
 }
