@@ -5,6 +5,7 @@ import os
 import re
 
 import pytest
+import torch
 
 from up_projection_b200 import _capi
 
@@ -53,3 +54,13 @@ def test_gate_rows_whose_bytes_wrap_are_refused(rows):
     p = _params(gate=a[6], rows=rows)
     assert lib.swiglu_block_norm(a[0], a[1], p, a[4], None, None, None, 0, 64, 0, None) == dim
     assert lib.swiglu_block_norm_bwd(*a[:6], p, a[8], a[9], None, None, a[10], None, 0, 0, 64, 0, None) == dim
+
+
+def test_gate_without_rows_is_refused():
+    """Its null address would read as no gate at all.  (CPU tensors stand for a
+    device's here: the check looks at shapes.)"""
+    g = torch.ones((0, 64))
+    assert g.data_ptr() == 0
+    with pytest.raises(ValueError, match="gate"):
+        _capi._norm_params(-1, torch.float32, 64, None, None, g, 1.0, 1e-6)
+    assert _capi._norm_params(-1, torch.float32, 64, None, None, torch.ones((2, 64)), 1.0, 1e-6).gate_rows == 2

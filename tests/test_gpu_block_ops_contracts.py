@@ -7,6 +7,7 @@ import block_ref as ref
 import up_projection_b200 as up
 from gpu_util import dev
 from test_gpu_block_ops import rand
+from up_projection_b200 import _capi
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,18 @@ def test_transposed_codes_behind_the_rows_are_zero(R, C, block, dtype):
     assert q.shape == (C, (R + 15) // 16 * 16)
     assert torch.equal(q, wq)
     assert torch.equal(torch.nan_to_num(s.double(), nan=-1.0), torch.nan_to_num(ws, nan=-1.0))
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("M", [0, 6])
+def test_gate_without_rows_is_refused(M, native, monkeypatch):
+    """A gate [0, D] is no gate row for any row, not a call without a gate."""
+    _capi.lib()
+    if not native:
+        monkeypatch.setattr(_capi, "_native", None)
+    x, g, w = (torch.ones((n, 64), device=dev()) for n in (M, 0, 1))
+    with pytest.raises(ValueError):
+        up.swiglu_block_norm(x, x, gate=g)
+    with pytest.raises(ValueError):
+        up.swiglu_block_norm_bwd(x, None, x, x, None, None, gate=g)
+    assert torch.equal(up.swiglu_block_norm(x, x, gate=w)[0], x + x)

@@ -614,11 +614,11 @@ def _norm_params(dev, dt, D, post_weight, pre_weight, gate, residual_scale, eps)
     if gate is not None:
         if gate.dim() == 2:
             rows = gate.shape[0]
-            ok = _fits(gate, dev, dt, (rows, D))
+            ok = rows > 0 and _fits(gate, dev, dt, (rows, D))
         else:
             ok = _fits(gate, dev, dt, (D,))
         if not ok:
-            _refuse(gate, "gate", f"[{D}] or [rows, {D}] of Y's dtype")
+            _refuse(gate, "gate", f"[{D}] or [rows, {D}] of Y's dtype, with a row at least")
         g = gate.data_ptr()
     return BlockNormParams(w1, w2, g, rows, residual_scale, eps)
 

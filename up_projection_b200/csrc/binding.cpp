@@ -125,6 +125,7 @@ struct Norm {
             gate = plain(ogate);
             if (!gate) return false;
             if (gate->dim() == 2) rows = gate->size(0);
+            if (rows == 0) return false;   // (its null address would read as no gate)
             if (gate->dim() == 2 ? !fits(gate, device, dtype, {rows, D}) : !fits(gate, device, dtype, {D}))
                 return false;
         }
