@@ -136,8 +136,8 @@ def lib() -> ctypes.CDLL:
 
 
 # csrc/binding.cpp: the calls of the operators around the projection that are in
-# order, done natively (None: not built for this torch, or not loaded yet).  A
-# native call returns None for what it leaves to the functions below.
+# order, done natively (None: not built, built for another torch, or not loaded
+# yet).  A native call returns None for what it leaves to the functions below.
 _native = None
 
 
@@ -145,8 +145,11 @@ def _bind(handle):
     global _native
     try:
         from . import _binding
+        from .build import binding_stamp
     except ImportError:
         return
+    if getattr(_binding, "built_for", None) != binding_stamp():
+        return  # its inlined tensor code is another torch's
     _binding.bind(*(ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in (
         "swiglu_block_norm", "swiglu_block_norm_bwd_workspace", "swiglu_block_norm_bwd",
         "swiglu_quant_b128", "swiglu_gemm_b128", "swiglu_fwd_b128")))

@@ -7,8 +7,9 @@ then linked into ``up_projection_b200/libswiglu_b200.so`` with the CUDA
 runtime linked statically, so the library needs only the driver at run time.
 ``-Xptxas -v`` output (registers, spills, shared memory per kernel) is kept
 in ``_build/ptxas.log``.  ``csrc/binding.cpp``, the native calls of the
-operators around the projection, becomes ``_binding.so`` next to it (g++, torch's
-headers); without it those calls go through ctypes.
+operators around the projection, becomes ``_binding<interpreter's suffix>`` next
+to it (g++, torch's headers); without it, or with one built for another torch,
+those calls go through ctypes.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libswiglu_b200.so")
-BINDING = os.path.join(PKG, "_binding.so")
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -55,23 +58,42 @@ def up_to_date() -> bool:
     return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
 
 
+def binding_stamp() -> str:
+    """What a binding is built for: this torch, its C++ ABI and this interpreter."""
+    import torch
+    return (f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"python {sysconfig.get_config_var('SOABI')}")
+
+
+def _stamp_file() -> str:
+    return os.path.join(BUILD, "binding.stamp")
+
+
 def binding_up_to_date() -> bool:
     deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "swiglu.h"), os.path.abspath(__file__)]
-    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(f) for f in deps)
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(os.path.getmtime(f) for f in deps):
+        return False
+    try:
+        with open(_stamp_file()) as f:
+            return f.read() == binding_stamp()
+    except OSError:
+        return False
 
 
 def build_binding(force: bool = False) -> str:
     """Compile csrc/binding.cpp against this interpreter and its torch."""
     if not force and binding_up_to_date():
         return BINDING
-    import sysconfig
-
+    # nothing built for another interpreter or torch is left to be imported
+    for old in glob.glob(os.path.join(os.path.dirname(BINDING), "_binding*.so")):
+        os.remove(old)
     import torch
-    base = os.path.join(os.path.dirname(torch.__file__))
+    base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BINDING + f".tmp{os.getpid()}"
+    stamp = binding_stamp()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DSWIGLU_BUILT_FOR="{stamp}"',
            f"-I{INCLUDE}", "-I" + sysconfig.get_paths()["include"], f"-I{base}/include",
            f"-I{base}/include/torch/csrc/api/include", f"-I{cuda}/include",
            os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{base}/lib", "-ltorch_python", "-ltorch",
@@ -80,6 +102,9 @@ def build_binding(force: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError("binding failed:\n" + p.stdout + p.stderr)
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(_stamp_file(), "w") as f:
+        f.write(stamp)
     return BINDING
 
 
@@ -91,9 +116,17 @@ def _compile(src: str):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
-    if not force and up_to_date():
-        return LIB
+    """The library, then the binding, whose failure is a warning."""
+    if force or not up_to_date():
+        _build_library(verbose)
+    try:
+        build_binding(force)
+    except Exception as e:  # no compiler, no headers, a torch it does not fit
+        warnings.warn(f"no native binding, its calls go through ctypes: {e}")
+    return LIB
+
+
+def _build_library(verbose: bool):
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     logs = []
@@ -117,7 +150,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError("link failed:\n" + p.stdout + p.stderr)
     os.replace(tmp, LIB)
-    return LIB
 
 
 def main(argv=None):

@@ -371,4 +371,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Native calls of the op
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// (SWIGLU_BUILT_FOR: the torch, ABI and interpreter of these headers, which the
+// importer compares with its own before the first call)
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", SWIGLU_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
