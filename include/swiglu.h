@@ -392,10 +392,15 @@ SWIGLU_API int swiglu_quant_b128(const void *X, void *Q, float *S, int64_t R, in
  *  With X, W, dY quantised by swiglu_quant_b128, a linear layer Y = X W^T is
  *  (X, W tile), its input gradient (dY, W tile transposed) and its weight
  *  gradient (dY transposed, X transposed, b_block ROW).
- *  Each block's products accumulate in fp32 on the tensor cores; the scaled
- *  blocks are summed in fp32 with round-to-nearest adds in block order; one
- *  rounding to out_dtype.  Any fp32 scales are taken as they are (negative,
- *  zero, NaN and Inf follow the formula); NaN codes give NaN.
+ *  Each block's products accumulate in fp32 on the tensor cores and are added to
+ *  fp32 sums by a fused multiply-add with the factor As[m,b] Bs[n,b], which is
+ *  formed in fp32 first; one rounding to out_dtype.  Order of the blocks: for
+ *  many rows, b = 0, 1, ...; for few (M <= 32, or M <= 64 with K > 2048) up to
+ *  16 partial sums, of every other block of a run of blocks (M <= 32) or of the
+ *  whole run, joined in a fixed order.  A call's bits depend on its sizes and
+ *  the device only, but a row's may differ between calls of different M.
+ *  Any fp32 scales are taken as they are (negative, zero, NaN and Inf follow
+ *  the formula); NaN codes give NaN.
  *  M == 0 or N == 0: nothing enqueued.  K == 0: Y is set to +0.  Y must not
  *  overlap an input.  Allocates no device memory.
  */

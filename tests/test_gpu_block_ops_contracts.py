@@ -102,3 +102,45 @@ def test_gate_without_rows_is_refused(M, native, monkeypatch):
     with pytest.raises(ValueError):
         up.swiglu_block_norm_bwd(x, None, x, x, None, None, gate=g)
     assert torch.equal(up.swiglu_block_norm(x, x, gate=w)[0], x + x)
+
+
+def _one_product_per_block(M, N, kb, seed):
+    """Operands whose blocks hold one product 1 x 1 each, scaled by powers of
+    two of such different sizes that the order of the fp32 sums shows."""
+    one = torch.tensor(1.0, device=dev()).to(torch.float8_e4m3fn).view(torch.uint8)
+    A = torch.zeros((M, kb * 128), dtype=torch.uint8, device=dev())
+    B = torch.zeros((N, kb * 128), dtype=torch.uint8, device=dev())
+    A[:, ::128] = one
+    B[:, ::128] = one
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    sign = torch.randint(0, 2, (M, kb), generator=g, device="cuda").float() * 2 - 1
+    As = sign * torch.rand((M, kb), generator=g, device="cuda") * torch.exp2(
+        torch.randint(0, 30, (M, kb), generator=g, device="cuda").float())
+    return A, ref.row_scales(As), B
+
+
+@pytest.mark.parametrize("M", [65, 300])
+@pytest.mark.parametrize("block", ["tile", "row"])
+def test_many_rows_add_their_blocks_in_order(M, block):
+    N, kb = 136, 19
+    A, As, B = _one_product_per_block(M, N, kb, M)
+    Bs = torch.ones((2, kb), device=dev()) if block == "tile" else ref.row_scales(torch.ones((N, kb), device=dev()))
+    Y = up.swiglu_gemm_b128(A, As, B, Bs, out_dtype=torch.float32)
+    want = torch.zeros((M,), device=dev())
+    for b in range(kb):
+        want = want + As[:, b]
+    assert torch.equal(Y, want[:, None].expand(M, N))
+    assert not torch.equal(As.double().sum(1).float(), want)    # (the order does show)
+
+
+@pytest.mark.parametrize("M", [1, 8, 20, 32, 33, 64])
+def test_few_rows_give_the_same_bits_every_time(M):
+    N, kb = 520, 40
+    A, As, B = _one_product_per_block(M, N, kb, M)
+    Bs = torch.ones(((N + 127) // 128, kb), device=dev())
+    Y = [up.swiglu_gemm_b128(A, As, B, Bs, out_dtype=torch.float32) for _ in range(4)]
+    assert all(torch.equal(y, Y[0]) for y in Y)
+    # each partial sum and each join is off by half a unit of at most the terms' sum
+    bound = kb * 2.0 ** -24 * As.double().abs().sum(1)
+    assert bool(((Y[0].double() - As.double().sum(1)[:, None]).abs() <= bound[:, None]).all())

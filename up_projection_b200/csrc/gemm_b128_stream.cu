@@ -68,7 +68,7 @@ struct StreamPlan {
     int nrt;           // MMAs per step: groups of mma_m rows of them
     int a_rows;        // rows of an A box
     int mma_n;
-    int tok;           // rows of A per accumulating warp: 8, 32, 64
+    int tok;           // rows of A per accumulating warp: 8 or 32
     int parity;        // the two warps of a row take every other block
     int kbs, g;        // blocks per stage, per TMEM buffer
     int acc_cols;      // TMEM columns of a block and group of 128 rows
