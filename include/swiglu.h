@@ -400,7 +400,9 @@ SWIGLU_API int swiglu_quant_b128(const void *X, void *Q, float *S, int64_t R, in
  *  whole run, joined in a fixed order.  A call's bits depend on its sizes and
  *  the device only, but a row's may differ between calls of different M.
  *  Any fp32 scales are taken as they are (negative, zero, NaN and Inf follow
- *  the formula); NaN codes give NaN.
+ *  the formula) whose products As[m,b] Bs[n,b] stay in the range of fp32: one
+ *  beyond it counts as infinite, also where the block's sum is 0, and one below
+ *  the subnormals as 0.  NaN codes give NaN.
  *  M == 0 or N == 0: nothing enqueued.  K == 0: Y is set to +0.  Y must not
  *  overlap an input.  Allocates no device memory.
  */

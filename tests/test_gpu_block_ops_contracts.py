@@ -144,3 +144,21 @@ def test_few_rows_give_the_same_bits_every_time(M):
     # each partial sum and each join is off by half a unit of at most the terms' sum
     bound = kb * 2.0 ** -24 * As.double().abs().sum(1)
     assert bool(((Y[0].double() - As.double().sum(1)[:, None]).abs() <= bound[:, None]).all())
+
+
+@pytest.mark.parametrize("M", [4, 40, 200])
+def test_scales_meet_before_the_sums(M):
+    """Far apart, the scales' product is what counts; beyond fp32's range it is
+    infinite, below the subnormals zero."""
+    N, kb = 136, 17
+    A, _, B = _one_product_per_block(M, N, kb, 0)
+    a, b = torch.ones((M, kb), device=dev()), torch.ones((2, kb), device=dev())
+    a[:, 3], b[:, 3] = 2.0 ** 110, 2.0 ** -108
+    a[:, 4], b[:, 4] = 2.0 ** -120, 2.0 ** 121
+    a[:, 5], b[:, 5] = 2.0 ** -100, 2.0 ** -100
+    Y = up.swiglu_gemm_b128(A, ref.row_scales(a), B, b, out_dtype=torch.float32)
+    assert bool((Y == kb - 3 + 4 + 2).all())
+    a[0, 7], b[0, 7] = 2.0 ** 100, 2.0 ** 100
+    A[0, 7 * 128] = 0                           # the block's sum is 0
+    Y = up.swiglu_gemm_b128(A, ref.row_scales(a), B, b, out_dtype=torch.float32)
+    assert bool(torch.isnan(Y[0, :128]).all()) and bool(torch.isfinite(Y[1:, 128:]).all())
