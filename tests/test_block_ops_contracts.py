@@ -7,6 +7,7 @@ import re
 import pytest
 import torch
 
+from test_host_plans import _build_and_run
 from up_projection_b200 import _capi
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "up_projection_b200", "csrc")
@@ -64,3 +65,13 @@ def test_gate_without_rows_is_refused():
     with pytest.raises(ValueError, match="gate"):
         _capi._norm_params(-1, torch.float32, 64, None, None, g, 1.0, 1e-6)
     assert _capi._norm_params(-1, torch.float32, 64, None, None, torch.ones((2, 64)), 1.0, 1e-6).gate_rows == 2
+
+
+def test_status_words_are_read_once_and_written_only_if_set():
+    """Each kernel file adds a word to swiglu_sync_status; a word that is clear
+    costs one read (status_check.cu)."""
+    _build_and_run(["tests/status_check.cu"], 6)
+    for n in sorted(os.listdir(CSRC)):
+        if n.endswith(".cu"):
+            code = _code(os.path.join(CSRC, n))
+            assert code.count("_status_fetch_and_clear(unsigned int *host_out") == code.count("return fetch_and_clear(g_"), n

@@ -533,33 +533,21 @@ SWIGLU_API int swiglu_sync_status(cudaStream_t stream) {
     if (st != SWIGLU_OK) return st;
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return from_cuda(e);
-    unsigned int w1 = 0, w2 = 0, w3 = 0, w4 = 0, w5 = 0, w6 = 0, w7 = 0, w8 = 0;
-    e = gemm_bf16_status_fetch_and_clear(&w1, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = gemm_tf32x3_status_fetch_and_clear(&w2, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = decode_status_fetch_and_clear(&w3, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = gemm_bwd_status_fetch_and_clear(&w4, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = gemm_bwd_tf32x3_status_fetch_and_clear(&w5, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = selftest_status_fetch_and_clear(&w6, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = stream_tc_status_fetch_and_clear(&w7, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    e = gemm_tf32x3_2sm_status_fetch_and_clear(&w8, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    unsigned int w9 = 0;
-    e = gemm_b128_status_fetch_and_clear(&w9, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    unsigned int w10 = 0;
-    e = gemm_b128_stream_status_fetch_and_clear(&w10, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    unsigned int w11 = 0;
-    e = block_norm_status_fetch_and_clear(&w11, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    return (w1 | w2 | w3 | w4 | w5 | w6 | w7 | w8 | w9 | w10 | w11) ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
+    constexpr cudaError_t (*kWords[])(unsigned int *, cudaStream_t) = {
+        gemm_bf16_status_fetch_and_clear,      gemm_tf32x3_status_fetch_and_clear,
+        decode_status_fetch_and_clear,         gemm_bwd_status_fetch_and_clear,
+        gemm_bwd_tf32x3_status_fetch_and_clear, selftest_status_fetch_and_clear,
+        stream_tc_status_fetch_and_clear,      gemm_tf32x3_2sm_status_fetch_and_clear,
+        gemm_b128_status_fetch_and_clear,      gemm_b128_stream_status_fetch_and_clear,
+        block_norm_status_fetch_and_clear};
+    unsigned int any = 0;
+    for (auto fetch : kWords) {
+        unsigned int word = 0;
+        e = fetch(&word, stream);
+        if (e != cudaSuccess) return from_cuda(e);
+        any |= word;
+    }
+    return any ? SWIGLU_ERR_TIMEOUT : SWIGLU_OK;
 }
 
 SWIGLU_API int swiglu_selftest_wait_timeout(cudaStream_t stream) {

@@ -23,6 +23,7 @@
 #include "kernels.cuh"
 #include "pdl.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 
 namespace swiglu {
 
@@ -1132,14 +1133,7 @@ cudaError_t launch_block_norm_bwd(const void *dRn, const void *dN, const void *Y
 }
 
 cudaError_t block_norm_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_block_norm_status, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_block_norm_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice,
-                                stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_block_norm_status, host_out, stream);
 }
 
 }  // namespace swiglu

@@ -44,6 +44,7 @@
 #include "gemm_common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 #include "tmap.cuh"
 
 namespace swiglu {
@@ -482,14 +483,7 @@ cudaError_t launch_decode_bf16(const void *X, const void *Wg, const void *Wu, vo
 }
 
 cudaError_t decode_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_decode_status, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_decode_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_decode_status, host_out, stream);
 }
 
 }  // namespace swiglu

@@ -41,6 +41,7 @@
 
 #include "b128.cuh"
 #include "kernels.cuh"
+#include "status.cuh"
 #include "tmap.cuh"
 
 namespace swiglu {
@@ -789,14 +790,7 @@ cudaError_t launch_fwd_b128_stream(const void *X, const float *Xs, const void *W
 }
 
 cudaError_t gemm_b128_stream_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_gemm_b128_stream_status, sizeof(unsigned int),
-                                              0, cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_gemm_b128_stream_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_gemm_b128_stream_status, host_out, stream);
 }
 
 }  // namespace swiglu

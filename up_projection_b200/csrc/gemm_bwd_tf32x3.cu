@@ -59,6 +59,7 @@
 #include "gemm_common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 #include "tf32x3.cuh"
 #include "tmap.cuh"
 
@@ -895,15 +896,7 @@ cudaError_t launch_bwd_all_tf32x3(const void *dG, const void *dU, const void *Wg
 }
 
 cudaError_t gemm_bwd_tf32x3_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_gemm_bwd_tf32x3_status,
-                                              sizeof(unsigned int), 0, cudaMemcpyDeviceToHost,
-                                              stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_gemm_bwd_tf32x3_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_gemm_bwd_tf32x3_status, host_out, stream);
 }
 
 }  // namespace swiglu

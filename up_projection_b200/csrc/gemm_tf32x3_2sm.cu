@@ -30,6 +30,7 @@
 #include "gemm_common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 #include "tf32x3.cuh"
 #include "tmap.cuh"
 
@@ -406,15 +407,7 @@ cudaError_t launch_gemm_tf32x3_2sm(const void *X, const void *Wg, const void *Wu
 }
 
 cudaError_t gemm_tf32x3_2sm_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_gemm_tf32x3_2sm_status,
-                                              sizeof(unsigned int), 0, cudaMemcpyDeviceToHost,
-                                              stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_gemm_tf32x3_2sm_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_gemm_tf32x3_2sm_status, host_out, stream);
 }
 
 }  // namespace swiglu

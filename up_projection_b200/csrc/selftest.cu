@@ -6,6 +6,7 @@
 // from swiglu_sync_status.
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 
 namespace swiglu {
 
@@ -36,14 +37,7 @@ cudaError_t launch_selftest_wait(long long limit_cycles, cudaStream_t stream) {
 }
 
 cudaError_t selftest_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_selftest_status, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_selftest_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_selftest_status, host_out, stream);
 }
 
 }  // namespace swiglu

@@ -45,6 +45,7 @@
 #include "gemm_common.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "status.cuh"
 #include "tmap.cuh"
 
 namespace swiglu {
@@ -616,14 +617,7 @@ cudaError_t launch_stream_tc_bf16(const void *X, const void *Wg, const void *Wu,
 }
 
 cudaError_t stream_tc_status_fetch_and_clear(unsigned int *host_out, cudaStream_t stream) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(host_out, g_stream_tc_status, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_stream_tc_status, &zero, sizeof(unsigned int), 0,
-                                cudaMemcpyHostToDevice, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+    return fetch_and_clear(g_stream_tc_status, host_out, stream);
 }
 
 }  // namespace swiglu
