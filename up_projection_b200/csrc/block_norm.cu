@@ -466,10 +466,12 @@ struct NormBwdArgs {
 // What is kept between the two passes over a row: with 16 elements a thread or
 // fewer, e and the products of the weights (in registers); with more they are
 // formed again, because the column sums alone fill half the registers.
-// D = 4096, bf16: M = 16384 137 us with the join, 90 % of the measured copy
-// bandwidth; M = 2048 29 us, 53 % (14 rows per block: filling the rings and
-// the join, 5 us, are a third of it).  One CTA-wide loop over rows read
-// straight from memory took 234 and 45 us: its loads waited for its barriers.
+// D = 4096, bf16, with the join: 7.6 ns per row (six rows of HBM at 6.5 TB/s)
+// and some 12 us at any M: the rings' fill, the column sums' way out and the
+// join, which launched by itself takes 5.4 us.  M = 16384 136 us, 91 % of the
+// measured copy bandwidth; M = 2048 28.4 us, 54 %.  One CTA-wide loop over rows
+// read straight from memory took 234 and 45 us: its loads waited for its
+// barriers.
 template <bool kBf16, int kV, bool kGates>
 __global__ void __launch_bounds__(kRingThreads, 1) block_norm_bwd_kernel(const NormBwdArgs a) {
     using E = Vec<kBf16>;

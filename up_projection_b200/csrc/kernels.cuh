@@ -184,12 +184,17 @@ cudaError_t launch_fwd_b128(const void *X, const float *Xs, const void *Wg, cons
                             const void *Wu, const float *Us, void *H, int M, int N, int K,
                             const Epilogue &epi, const DeviceInfo &dev, cudaStream_t stream);
 // Few rows (gemm_b128_stream.cu), reached through the two above.  Its time
-// grows with M, the large products' hardly does up to 256 rows; they meet
-// between 32 and 96 rows, later where the reduction is long (it is split over
-// SMs here only).  B200, both kernels, a call between two events, us: M = 96,
-// N = K = 4096 28.8 here, 20.5 there, gated 11008 x 4096 71.7 and 45.1; M = 64,
-// 4096 x 14336 36.9 and 49.2, 1024 x 1024 14.3 and 12.3, gated 6912 x 1536 22.5
-// and 18.4; M = 32, 4096 x 14336 32.8 and 47.1, gated 11008 x 4096 36.9 and 45.1.
+// grows with M, the large products' hardly does up to 256 rows; where they
+// meet depends on N and K, as the reduction is split over SMs here only.  B200,
+// weights out of HBM, us, here and there (there at one row more than the rule
+// takes):
+//   K > 2048, M = 33 to 64: 4096 x 14336 25.4 to 29.3 here, 41.5 there; gated
+//     11008 x 4096 32.0 to 32.9 and 34.8; but 4096 x 4096 15.6 to 19.6 and 14.9;
+//   K <= 2048, M = 32: gated 11008 x 2048 20.4 and 21.9, 11008 x 1024 14.9 and
+//     14.9, 6912 x 1536 12.3 and 12.2; but plain 4096 x 2048 10.4 and 9.9, 11008 x
+//     2048 13.2 and 11.4, 4096 x 1024 8.3 and 7.1, 11008 x 1024 10.0 and 8.1.
+// So the rule holds for long reductions and for the gated pair; for plain
+// products with K of 4096 or less it hands over late and costs up to a third.
 constexpr int kB128StreamMaxM = 64;
 inline bool b128_few_rows(int M, int K) { return M <= 32 || (M <= kB128StreamMaxM && K > 2048); }
 cudaError_t launch_gemm_b128_stream(const void *A, const float *As, const void *B, const float *Bs,
