@@ -70,6 +70,27 @@ def test_call_on_a_stream_that_captures_beside_the_current_one():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_call_on_another_stream_stays_out_of_a_capture():
+    """The current stream captures, the call's does not: it runs at once, and
+    the capture ends as it would without it."""
+    M, D = 64, 256
+    x, w = rand((M, D), 1, torch.bfloat16), rand((D,), 2, torch.bfloat16)
+    Rn, _, r1, r2 = up.swiglu_block_norm(x, x, w, w, return_stats=True)
+    want = up.swiglu_block_norm_bwd(x, x, x, Rn, r1, r2, w, w)
+    side = torch.cuda.Stream()
+    up.swiglu_block_norm_bwd(x, x, x, Rn, r1, r2, w, w, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = up.swiglu_block_norm_bwd(x, x, x, Rn, r1, r2, w, w, stream=side)
+        y = x + 1
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want) if b is not None)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, x + 1)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("block", ["row", "tile"])
 @pytest.mark.parametrize("R,C", [(1, 16), (5, 144), (121, 272), (130, 400), (250, 128), (268, 272)])

@@ -179,8 +179,9 @@ def _stream(stream) -> int:
 def _drawn(stream, *tensors) -> int:
     """The call's stream as a handle, after outputs and scratch were drawn on
     the current one.  Another stream first waits for what may still use their
-    memory there, and keeps it until its own work is done.  (A stream that
-    captures cannot wait for one that does not.)"""
+    memory there, and keeps it until its own work is done.  (Not where one of
+    the two captures: its memory is the graph's, and waiting would draw the
+    other in.)"""
     s = _stream(stream)
     if stream is None:
         return s
@@ -190,7 +191,7 @@ def _drawn(stream, *tensors) -> int:
             stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
         with torch.cuda.stream(stream):
             captures = torch.cuda.is_current_stream_capturing()
-        if not captures or torch.cuda.is_current_stream_capturing():
+        if captures == torch.cuda.is_current_stream_capturing():
             stream.wait_stream(current)
         for t in tensors:
             if t is not None:
