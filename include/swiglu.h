@@ -383,10 +383,11 @@ SWIGLU_API int swiglu_quant_b128(const void *X, void *Q, float *S, int64_t R, in
  *
  *  A   [M, K] device e4m3 codes, 16-byte aligned; K a multiple of 16.
  *  As  1 x 128 scales of A: [KB, M4], M4 = M rounded up to 4, block b of row
- *      m at As[b*M4 + m] (as swiglu_quant_b128 writes them).
+ *      m at As[b*M4 + m] (as swiglu_quant_b128 writes them), 16-byte aligned.
  *  B   [N, K] device e4m3 codes, 16-byte aligned; N a multiple of 8.
  *  Bs  b_block SWIGLU_BLOCK_TILE: [ceil(N/128), KB] (weights);
- *      SWIGLU_BLOCK_ROW: [KB, N], block b of row n at Bs[b*N + n].
+ *      SWIGLU_BLOCK_ROW: [KB, N], block b of row n at Bs[b*N + n]; 16-byte
+ *      aligned.
  *  Y   [M, N] device, out_dtype elements, 16-byte aligned; written only.
  *
  *  With X, W, dY quantised by swiglu_quant_b128, a linear layer Y = X W^T is
@@ -457,6 +458,7 @@ typedef struct swiglu_block_norm_params {
  *  rstd_post, rstd_pre  [M] device fp32, or NULL: r1 and r2, for the backward
  *      (each not used without its weight).
  *  D a multiple of 8 (bf16) / 4 (fp32), at most 16384 (bf16) / 8192 (fp32).
+ *  Every pointer is 16-byte aligned, those of the statistics too.
  *  M == 0 or D == 0: nothing enqueued.  Any other overlap of an output with
  *  an input or another output is SWIGLU_ERR_OVERLAP.  Allocates no device
  *  memory.
@@ -489,6 +491,7 @@ SWIGLU_API int64_t swiglu_block_norm_bwd_workspace(const swiglu_block_norm_param
  *  workspace  16-byte aligned device memory of at least the bytes
  *       swiglu_block_norm_bwd_workspace returns, scratch of this call alone
  *       (calls that may run at once need one each); NULL if that is 0.
+ *  Every pointer is 16-byte aligned, those of the statistics too.
  *  The column sums are fp32, summed in a fixed order (no atomics).  M == 0:
  *  d_post, d_pre and d_gate set to +0.  No output may overlap an input,
  *  another output or the workspace.
